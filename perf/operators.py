@@ -258,7 +258,7 @@ def _run_own(st):
         cider.cider_paged_append(st["k"], st["v"], st["k_cache"], st["v_cache"], st["slots"])
         return {"k_cache": st["k_cache"], "v_cache": st["v_cache"]}
     return cider.cider_paged_attention(st["q"], st["k_cache"], st["v_cache"], st["table"], st["cu"], st["kv_len"],
-                                       max_new=st["max_new"], window=st["window"], sinks=st["sinks"], out=st["out"],
+                                       max_fresh=st["max_new"], window=st["window"], sinks=st["sinks"], out=st["out"],
                                        workspace=st["workspace"])
 
 
