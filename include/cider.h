@@ -89,7 +89,10 @@ CIDER_API const char* cider_last_error(void);
 
 /* Synchronises `stream`, then reads and clears the device status word of the
  * current device: CIDER_OK, or CIDER_ERR_TIMEOUT if a bounded wait in some
- * kernel ran out since the last read.  Not for the hot path. */
+ * kernel ran out since the last read, or CIDER_ERR_INVALID_ARG if a paged-cache
+ * kernel met a length, page number or slot in device memory that its call does
+ * not allow (each entry point says what it does with such a value; none of
+ * them reads or writes outside the caller's buffers).  Not for the hot path. */
 CIDER_API cider_status_t cider_device_status(void* stream);
 
 /* Bytes of workspace the linear entry points need for M tokens of K inputs:
@@ -318,7 +321,106 @@ CIDER_API cider_status_t cider_sdpa_decode(const void* q, const void* k, const v
                                  int64_t H_q, int64_t H_kv, int64_t N, int64_t D, void* out,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- paged key/value cache ------------------------------------------------
+ * Keys and values of many requests in one pool of fixed-size pages, and the
+ * attention of every request's new tokens over them: a decode token, a chunk
+ * of a prompt, or a batch of both.  The pages' decode attention above takes
+ * one request whose cache is contiguous; these calls are its form for a
+ * server's batch (an addition of this library).  All lengths, tables and slots
+ * are int32 arrays in device memory, so a step needs no host round trip and
+ * can be captured in a CUDA graph and replayed with other lengths. */
+
+/* The cache: element (page, head, token in page, d) of K is at
+ *   k + page * stride_page + head * stride_head + token * stride_token + d
+ * (strides in elements), V likewise from v with the same strides.  So
+ * [num_pages][H_kv][page_size][D] and [num_pages][page_size][H_kv][D] are both
+ * taken.  dt: fp16 or bf16; D: 64 or 128; page_size: 16, 32, 64, 128 or 256;
+ * num_pages * page_size < 2^31; H_kv <= 65535; strides multiples of 8 under
+ * which no two elements share an address; k and v 16-byte aligned. */
+typedef struct {
+    void* k;
+    void* v;
+    cider_dtype_t dt;
+    int64_t num_pages, page_size, H_kv, D;
+    int64_t stride_page, stride_head, stride_token;
+} cider_paged_cache_t;
+
+/* Block tables, slots and offsets of one step, from the requests' lengths.
+ * Request b has cached[b] tokens in the cache and fresh[b] new ones.  Its
+ * position j lives in page block_table[b * ld_table + j / page_size], at
+ * offset j % page_size.  The call
+ *  - takes need[b] = ceil((cached + fresh) / ps) - ceil(cached / ps) pages from
+ *    free_pages, the requests one after another (request b gets
+ *    free_pages[s .. s + need[b]), s = the sum of need over the requests before
+ *    it), and writes them into its table behind the pages that it has;
+ *  - writes cu_fresh[0 .. B] (prefix sums of fresh), kv_len[b] = cached + fresh,
+ *    slots[0 .. rows) (new token t of the packed batch goes to slot
+ *    page * page_size + offset; -1 for t >= cu_fresh[B]) and taken[0] = the
+ *    sum of need.
+ * 1 <= B <= 4096; 0 <= rows < 2^31; 1 <= width <= ld_table, width * page_size
+ * <= 2^30; num_free >= 0 (free_pages may be NULL if it is 0);
+ * num_pages * page_size < 2^31.  slots may be NULL if rows is 0.  Outputs must
+ * not overlap inputs or each other.
+ * In device memory, reported by cider_device_status(): a negative length
+ * counts as 0; a request longer than its table stops at the table's end
+ * (kv_len, too; its tokens behind that get slot -1); where free_pages runs out
+ * or holds a page outside [0, num_pages), the table entry is -1; tokens of a
+ * page outside [0, num_pages) get slot -1; tokens behind `rows` get no slot.
+ * The call's sums stop at 2^31 - 1. */
+CIDER_API cider_status_t cider_paged_tables(const int32_t* cached, const int32_t* fresh, int64_t B,
+                                            const int32_t* free_pages, int64_t num_free, int64_t num_pages,
+                                            int64_t page_size, int32_t* block_table, int64_t ld_table, int64_t width,
+                                            int32_t* cu_fresh, int32_t* kv_len, int32_t* slots, int64_t rows,
+                                            int32_t* taken, void* stream);
+
+/* Writes T tokens' keys and values into their slots.  k_new, v_new: T rows of
+ * [H_kv][D] in the cache's dt, token t at k_new + t * ld_k (v_new + t * ld_v)
+ * elements, so slices of a fused projection's output are taken as they are:
+ * ld_k, ld_v multiples of 8, at least H_kv * D (for T > 1).  slots: [T] int32;
+ * -1 skips the token, any other slot outside [0, num_pages * page_size) is
+ * skipped and reported by cider_device_status().  Two tokens with the same
+ * slot: which one's values remain is not defined.  k and v of the cache must
+ * differ; k_new and v_new must not overlap it. */
+CIDER_API cider_status_t cider_paged_append(const cider_paged_cache_t* cache, const void* k_new, int64_t ld_k,
+                                            const void* v_new, int64_t ld_v, const int32_t* slots, int64_t T,
+                                            void* stream);
+
+/* Attention of every request's new tokens over its pages (which hold the new
+ * tokens already).  Request b's queries are rows cu_fresh[b] .. cu_fresh[b+1]
+ * of q, the i-th of n at position p = kv_len[b] - n + i; query head h reads KV
+ * head h / (H_q / H_kv).  A query sees key j iff
+ *   j <= p, and, if window > 0, also j > p - window or j < sinks;
+ *   out = sum_j softmax_j(scale * q . K[j]) V[j] over the keys it sees.
+ * The sums, the softmax's maximum and its sum are fp32; the weights are rounded
+ * to dt before the product with V (each by at most half a unit, as an output
+ * is); the result is rounded once more.  A query with p < 0 (more new tokens
+ * than keys) sees nothing: its output is 0.  Keys that a query does not see
+ * have no effect on it, whatever they hold, NaN and infinities among it; keys
+ * that no query of a request sees are not read, and need no valid page.
+ * q: T rows of [H_q][D] at row stride ld_q; out: the same at ld_out (multiples
+ * of 8, at least H_q * D for T > 1); rows of out behind cu_fresh[B] are left
+ * as they are.  max_fresh: a bound on the new tokens of any one request (T is
+ * always one), by which the kernel is chosen; a bound that does not hold costs
+ * time, not correctness.  0 <= T <= 2^30 / (H_q / H_kv); 1 <= B <= 4096;
+ * window, sinks >= 0 and < 2^30; scale finite and > 0.
+ * workspace: cider_paged_attention_workspace_bytes(...) bytes, 16-byte aligned.
+ * In device memory, reported by cider_device_status(): cu_fresh outside [0, T]
+ * or decreasing is cut to it; kv_len outside [0, width * page_size] is cut to
+ * it; keys of a page outside [0, num_pages) count as not seen. */
+CIDER_API size_t cider_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t H_q, int64_t H_kv, int64_t D,
+                                                       int64_t max_fresh);
+CIDER_API cider_status_t cider_paged_attention(const cider_paged_cache_t* cache, const void* q, int64_t ld_q, int64_t T,
+                                               int64_t H_q, const int32_t* cu_fresh, const int32_t* kv_len, int64_t B,
+                                               const int32_t* block_table, int64_t ld_table, int64_t width,
+                                               int64_t max_fresh, int64_t window, int64_t sinks, float scale, void* out,
+                                               int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- test exports (stable, but not part of the operation's interface) ---- */
+/* Selects the paged-attention kernel for later calls (process-wide): 0 =
+ * automatic (default), 1 = the 16-row kernel, 2 = the tensor-core tile kernel.
+ * Query the workspace size after setting it.  Outside [0, 2]:
+ * CIDER_ERR_INVALID_ARG, nothing changes. */
+CIDER_API cider_status_t cider_test_set_paged_kernel(int kernel);
 /* The tcgen05 GEMM with an INT32 store epilogue: acc[m][n] = sum_k q[m,k]*w[n,k]. */
 CIDER_API cider_status_t cider_test_gemm_i32(const int8_t* q, const int8_t* w, int64_t M, int64_t N,
                                    int64_t K, int32_t* acc, void* stream);

@@ -74,6 +74,12 @@ _SIGNATURES = {
     "cider_test_set_small_m_kernel": (_INT, [_INT]),
     "cider_test_set_sdpa_kernel": (_INT, [_INT]),
     "cider_test_bounded_wait": (_INT, [_I64, _P]),
+    "cider_paged_tables": (_INT, [_P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
+    "cider_paged_append": (_INT, [_P, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "cider_paged_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "cider_paged_attention": (_INT, [_P, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64,
+                                     ctypes.c_float, _P, _I64, _P, _SZ, _P]),
+    "cider_test_set_paged_kernel": (_INT, [_INT]),
 }
 EXPORTS = tuple(_SIGNATURES)
 
@@ -439,6 +445,153 @@ def cider_test_set_gemm_variant(variant: int):
     """0 automatic, 1 single-CTA 128x128, 2 single-CTA 128x256, 3 CTA-pair 256x256, 4 single-CTA 128x80,
     5 CTA-pair 256x192."""
     _check("cider_test_set_gemm_variant", lib().cider_test_set_gemm_variant(variant))
+
+
+# ---- paged key/value cache -------------------------------------------------
+
+class _PagedCache(ctypes.Structure):  # cider_paged_cache_t
+    _fields_ = [("k", _P), ("v", _P), ("dt", _INT), ("num_pages", _I64), ("page_size", _I64), ("H_kv", _I64),
+                ("D", _I64), ("stride_page", _I64), ("stride_head", _I64), ("stride_token", _I64)]
+
+
+def _paged_cache(k_cache, v_cache):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or \
+            k_cache.dtype != v_cache.dtype or k_cache.stride(3) != 1:
+        raise ValueError("k_cache and v_cache are [num_pages, H_kv, page_size, D] of one dtype, with the same strides "
+                         "and unit stride along D")
+    P, H, S, D = k_cache.shape
+    sp, sh, st, _ = k_cache.stride()
+    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _DT[k_cache.dtype], P, S, H, D, sp, sh, st)
+
+
+def _paged_stream(device, stream, tensors):
+    """Checks that every tensor is on `device` and returns the stream's handle."""
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: one device is needed")
+    return _stream(stream, device)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream` (None: the current one): taken from that
+    stream's pool, so that what was freed on another one is not reused early."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _i32(t, name):
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name} must be int32")
+    return _contig(t, name)
+
+
+def _packed(t, name, heads, D):
+    """[T, heads, D] with dense rows -> its row stride."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} is [T, {heads}, {D}] with dense rows (any row stride)")
+    return t.stride(0)
+
+
+def cider_paged_tables(cached, fresh, free_pages, block_table, page_size, num_pages, rows, cu_fresh=None, kv_len=None,
+                       slots=None, taken=None, stream=None):
+    """Block tables and slots of one step.  cached, fresh: int32 [B] tokens that
+    each request has in the cache and brings; free_pages: int32 pages, taken in
+    order; block_table: int32 [B, width], filled behind the pages that each
+    request has; rows: rows of the packed batch.
+    -> (cu_fresh [B + 1], kv_len [B], slots [rows], taken [1]), all int32."""
+    dev = block_table.device
+    B = cached.shape[0]
+    if fresh.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1 or \
+            block_table.dtype != torch.int32:
+        raise ValueError("cached and fresh are [B], block_table is int32 [B, width] with dense rows")
+    if cu_fresh is None:
+        cu_fresh = _empty((B + 1,), torch.int32, dev, stream)
+    if kv_len is None:
+        kv_len = _empty((B,), torch.int32, dev, stream)
+    if slots is None:
+        slots = _empty((rows,), torch.int32, dev, stream)
+    if taken is None:
+        taken = _empty((1,), torch.int32, dev, stream)
+    if cu_fresh.numel() != B + 1 or kv_len.numel() != B or slots.numel() != rows or taken.numel() != 1:
+        raise ValueError("cu_fresh is [B + 1], kv_len [B], slots [rows] and taken [1]")
+    for t, name in ((cached, "cached"), (fresh, "fresh"), (free_pages, "free_pages"), (cu_fresh, "cu_fresh"),
+                    (kv_len, "kv_len"), (slots, "slots"), (taken, "taken")):
+        _i32(t, name)
+    st = _paged_stream(dev, stream, (cached, fresh, free_pages, cu_fresh, kv_len, slots, taken))
+    with torch.cuda.device(dev):
+        _check("cider_paged_tables", lib().cider_paged_tables(
+            cached.data_ptr(), fresh.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(), num_pages, page_size,
+            block_table.data_ptr(), block_table.stride(0), block_table.shape[1], cu_fresh.data_ptr(), kv_len.data_ptr(),
+            slots.data_ptr(), rows, taken.data_ptr(), st))
+    return cu_fresh, kv_len, slots, taken
+
+
+def cider_paged_append(k_new, v_new, k_cache, v_cache, slots, stream=None):
+    """Writes new keys and values ([T, H_kv, D], any row stride) into the cache
+    ([num_pages, H_kv, page_size, D], any strides) at slots (int32 [T]; -1
+    skips)."""
+    cache = _paged_cache(k_cache, v_cache)
+    if k_new.dtype != k_cache.dtype or v_new.dtype != k_cache.dtype:
+        raise ValueError("k_new, v_new and the cache must have one dtype")
+    ld_k, ld_v = (_packed(t, n, cache.H_kv, cache.D) for t, n in ((k_new, "k_new"), (v_new, "v_new")))
+    T = k_new.shape[0]
+    if v_new.shape[0] != T or slots.shape != (T,):
+        raise ValueError("k_new, v_new and slots must have the same number of rows")
+    st = _paged_stream(k_cache.device, stream, (v_cache, k_new, v_new, _i32(slots, "slots")))
+    with torch.cuda.device(k_cache.device):
+        _check("cider_paged_append", lib().cider_paged_append(
+            ctypes.addressof(cache), k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v, slots.data_ptr(), T, st))
+
+
+def cider_paged_attention_workspace_bytes(T, B, H_q, H_kv, D, max_fresh) -> int:
+    return int(lib().cider_paged_attention_workspace_bytes(T, B, H_q, H_kv, D, max_fresh))
+
+
+def cider_paged_attention(q, k_cache, v_cache, block_table, cu_fresh, kv_len, max_fresh=None, window=0, sinks=0,
+                          scale=None, out=None, workspace=None, stream=None):
+    """Causal attention of every request's new tokens over its pages.  q [T,
+    H_q, D] (any row stride), caches [num_pages, H_kv, page_size, D] (any
+    strides, the new tokens already in them), block_table int32 [B, width],
+    cu_fresh int32 [B + 1], kv_len int32 [B].  max_fresh: a bound on the new
+    tokens of any one request (default: T).  window > 0: a query sees the last
+    `window` keys up to its own, and the first `sinks`.  scale: default
+    1 / sqrt(D).  -> out [T, H_q, D]; rows behind the last request are left as
+    they are."""
+    cache = _paged_cache(k_cache, v_cache)
+    T, H_q, D = q.shape
+    ld_q = _packed(q, "q", H_q, cache.D)
+    if out is None:
+        out = _empty((T, H_q, D), q.dtype, q.device, stream)
+    ld_out = _packed(out, "out", H_q, cache.D)
+    if out.shape != q.shape or q.dtype != k_cache.dtype or out.dtype != q.dtype:
+        raise ValueError("q, out and the cache must have one dtype, and out q's shape")
+    B = kv_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1 or \
+            block_table.dtype != torch.int32 or cu_fresh.numel() != B + 1:
+        raise ValueError("block_table is int32 [B, width] with dense rows, cu_fresh [B + 1], kv_len [B]")
+    if max_fresh is None:
+        max_fresh = T
+    dev = q.device
+    st = _paged_stream(dev, stream, (k_cache, v_cache, block_table, _i32(cu_fresh, "cu_fresh"), _i32(kv_len, "kv_len"), out))
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = cider_paged_attention_workspace_bytes(T, B, H_q, cache.H_kv, D, max_fresh)
+            workspace = _empty((max(need, 16),), torch.uint8, dev, stream)
+        elif workspace.device != dev:
+            raise ValueError(f"tensors on {dev} and {workspace.device}: one device is needed")
+        _check("cider_paged_attention", lib().cider_paged_attention(
+            ctypes.addressof(cache), q.data_ptr(), ld_q, T, H_q, cu_fresh.data_ptr(), kv_len.data_ptr(), B,
+            block_table.data_ptr(), block_table.stride(0), block_table.shape[1], max_fresh, window, sinks,
+            D ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st))
+    return out
+
+
+def cider_test_set_paged_kernel(kernel: int):
+    """0 automatic, 1 the 16-row kernel, 2 the tensor-core tile kernel (process-wide)."""
+    _check("cider_test_set_paged_kernel", lib().cider_test_set_paged_kernel(kernel))
 
 
 def cider_test_set_sdpa_kernel(kernel: int):

@@ -13,11 +13,13 @@
 
 #include "../../include/cider.h"
 #include "cider_kernels.h"
+#include "paged.h"
 #include "sdpa_decode.h"
 
 namespace cider {
 
-// Device status word: bit 0 = a bounded wait ran out (kStatusTimeout).
+// Device status word: bit 0 = a bounded wait ran out (kStatusTimeout), bit 1 =
+// a paged-cache kernel met a value outside its range (kStatusIndex).
 __device__ unsigned g_status_word;
 
 namespace {
@@ -417,6 +419,9 @@ cider_status_t cider_device_status(void* stream) {
         if ((e = cudaMemcpy(d->status, &zero, sizeof zero, cudaMemcpyHostToDevice)) != cudaSuccess)
             return cuda_fail(e, "clearing the status word");
         if (v & kStatusTimeout) return fail(CIDER_ERR_TIMEOUT, "a bounded device-side wait ran out");
+        if (v & kStatusIndex)
+            return fail(CIDER_ERR_INVALID_ARG,
+                        "a paged-cache call met a length, page number or slot in device memory outside its range");
     }
     return CIDER_OK;
 }
@@ -738,6 +743,223 @@ cider_status_t cider_sdpa_decode(const void* q, const void* k, const void* v, ci
                                        static_cast<int>(N), plan, static_cast<float*>(workspace), out, d->status,
                                        static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CIDER_OK : cuda_fail(e, "decode-attention launch");
+}
+
+// ---- paged key/value cache ------------------------------------------------------
+namespace {
+constexpr int64_t kMaxLen = int64_t(1) << 30;     // keys of a request, window, sinks, rows x heads of a group
+constexpr int64_t kMaxStride = int64_t(1) << 36;  // elements; the tensor maps' byte strides stay below 2^40
+std::atomic<int> g_paged_kernel{0};               // test override: 0 automatic, 1 16-row tiles, 2 tensor-core tiles
+
+int log2_page(int64_t ps) {
+    for (int l = 4; l <= 8; ++l)
+        if (ps == (int64_t(1) << l)) return l;
+    return -1;
+}
+
+cider_status_t check_page_size(int64_t page_size, int64_t num_pages) {
+    if (log2_page(page_size) < 0)
+        return fail(CIDER_ERR_INVALID_ARG, "page_size = %lld must be 16, 32, 64, 128 or 256", (long long)page_size);
+    if (num_pages < 1 || num_pages > INT32_MAX / page_size)
+        return fail(CIDER_ERR_INVALID_ARG, "num_pages = %lld: 1 <= num_pages * page_size < 2^31", (long long)num_pages);
+    return CIDER_OK;
+}
+
+// Row stride of a [rows][width] array of 16-bit elements.
+cider_status_t check_ld(const char* name, int64_t ld, int64_t width, int64_t rows) {
+    if (rows > 1 && (ld < width || ld % 8 || ld > kMaxStride))
+        return fail(CIDER_ERR_INVALID_ARG, "%s = %lld must be a multiple of 8, at least %lld and at most 2^36", name,
+                    (long long)ld, (long long)width);
+    return CIDER_OK;
+}
+size_t row_span(int64_t rows, int64_t ld, int64_t width) {
+    return rows < 1 ? 0 : (static_cast<size_t>(rows - 1) * (rows > 1 ? ld : 0) + width) * 2;
+}
+
+// Checks the cache and gives it as the kernels take it, with the bytes it spans.
+cider_status_t check_cache(const cider_paged_cache_t* c, PagedCache* out, size_t* span) {
+    if (!c) return fail(CIDER_ERR_INVALID_ARG, "NULL cache");
+    if (c->dt != CIDER_F16 && c->dt != CIDER_BF16) return fail(CIDER_ERR_INVALID_ARG, "cache dtype %d unknown", (int)c->dt);
+    if (c->D != 64 && c->D != 128) return fail(CIDER_ERR_INVALID_ARG, "D = %lld must be 64 or 128", (long long)c->D);
+    if (c->H_kv < 1 || c->H_kv > 65535) return fail(CIDER_ERR_INVALID_ARG, "H_kv = %lld outside [1, 65535]", (long long)c->H_kv);
+    cider_status_t s = check_page_size(c->page_size, c->num_pages);
+    if (s != CIDER_OK) return s;
+    if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))
+        return fail(CIDER_ERR_INVALID_ARG, "the cache's k and v must be non-NULL and 16-byte aligned");
+    // from the innermost stride out, each dimension steps over what the ones inside it span
+    struct Dim {
+        int64_t n, stride;
+    } d[3] = {{c->num_pages, c->stride_page}, {c->H_kv, c->stride_head}, {c->page_size, c->stride_token}};
+    std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    int64_t inner = c->D;  // elements spanned so far
+    for (const Dim& x : d) {
+        if (x.n == 1) continue;
+        if (x.stride < inner || x.stride % 8 || x.stride > kMaxStride)
+            return fail(CIDER_ERR_INVALID_ARG,
+                        "cache strides must be multiples of 8, at most 2^36, and keep the elements apart (stride %lld, "
+                        "%lld elements inside it)", (long long)x.stride, (long long)inner);
+        if (x.stride > (int64_t(1) << 60) / x.n) return fail(CIDER_ERR_INVALID_ARG, "the cache spans more than 2^60 elements");
+        inner += (x.n - 1) * x.stride;
+    }
+    *span = static_cast<size_t>(inner) * 2;
+    *out = PagedCache{static_cast<char*>(c->k), static_cast<char*>(c->v), c->dt == CIDER_BF16 ? 1 : 0,
+                      static_cast<int>(c->num_pages), static_cast<int>(c->page_size), log2_page(c->page_size),
+                      static_cast<int>(c->H_kv), static_cast<int>(c->D), c->num_pages > 1 ? c->stride_page : 0,
+                      c->H_kv > 1 ? c->stride_head : 0, c->stride_token};
+    return CIDER_OK;
+}
+
+cider_status_t check_paged_attn(int64_t T, int64_t B, int64_t H_q, int64_t H_kv, int64_t D, int64_t max_fresh) {
+    if (D != 64 && D != 128) return fail(CIDER_ERR_INVALID_ARG, "D = %lld must be 64 or 128", (long long)D);
+    if (H_kv < 1 || H_kv > 65535 || H_q < 1 || H_q > 65535 || H_q % H_kv)
+        return fail(CIDER_ERR_INVALID_ARG, "H_q = %lld must be a positive multiple of H_kv = %lld, at most 65535", (long long)H_q,
+                    (long long)H_kv);
+    if (B < 1 || B > kPagedMaxRequests) return fail(CIDER_ERR_INVALID_ARG, "B = %lld outside [1, %d]", (long long)B, kPagedMaxRequests);
+    if (T < 0 || T > kMaxLen / (H_q / H_kv))
+        return fail(CIDER_ERR_INVALID_ARG, "T = %lld outside [0, 2^30 / (H_q / H_kv)]", (long long)T);
+    if (max_fresh < 0) return fail(CIDER_ERR_INVALID_ARG, "max_fresh = %lld must be >= 0", (long long)max_fresh);
+    return CIDER_OK;
+}
+}  // namespace
+
+cider_status_t cider_paged_tables(const int32_t* cached, const int32_t* fresh, int64_t B, const int32_t* free_pages,
+                                  int64_t num_free, int64_t num_pages, int64_t page_size, int32_t* block_table,
+                                  int64_t ld_table, int64_t width, int32_t* cu_fresh, int32_t* kv_len, int32_t* slots,
+                                  int64_t rows, int32_t* taken, void* stream) {
+    t_last_error[0] = '\0';
+    cider_status_t s = check_page_size(page_size, num_pages);
+    if (s != CIDER_OK) return s;
+    if (B < 1 || B > kPagedMaxRequests) return fail(CIDER_ERR_INVALID_ARG, "B = %lld outside [1, %d]", (long long)B, kPagedMaxRequests);
+    if (num_free < 0 || num_free > INT32_MAX) return fail(CIDER_ERR_INVALID_ARG, "num_free = %lld outside [0, 2^31)", (long long)num_free);
+    if (rows < 0 || rows > INT32_MAX) return fail(CIDER_ERR_INVALID_ARG, "rows = %lld outside [0, 2^31)", (long long)rows);
+    if (width < 1 || width > kMaxLen / page_size || (B > 1 && ld_table < width) || (B > 1 && ld_table > kMaxStride))
+        return fail(CIDER_ERR_INVALID_ARG, "width = %lld, ld_table = %lld: 1 <= width <= ld_table, width * page_size <= 2^30",
+                    (long long)width, (long long)ld_table);
+    if (!cached || !fresh || !block_table || !cu_fresh || !kv_len || !taken || (rows && !slots) || (num_free && !free_pages))
+        return fail(CIDER_ERR_INVALID_ARG, "NULL pointer");
+    const size_t nb = static_cast<size_t>(B) * 4;
+    const Range in[3] = {rng(cached, nb), rng(fresh, nb), rng(free_pages, static_cast<size_t>(num_free) * 4)};
+    const Range out[5] = {rng(block_table, (static_cast<size_t>(B - 1) * (B > 1 ? ld_table : 0) + width) * 4),
+                          rng(cu_fresh, nb + 4), rng(kv_len, nb), rng(slots, static_cast<size_t>(rows) * 4), rng(taken, 4)};
+    for (int i = 0; i < 5; ++i) {
+        if (out[i].lo & 3u) return fail(CIDER_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
+        for (const Range& r : in) {
+            if (r.lo & 3u) return fail(CIDER_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
+            if (overlap(out[i], r)) return fail(CIDER_ERR_INVALID_ARG, "an output overlaps an input");
+        }
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return fail(CIDER_ERR_INVALID_ARG, "two outputs overlap");
+    }
+    DeviceInfo* d = nullptr;
+    if ((s = device_info(&d)) != CIDER_OK) return s;
+    const PagedTablesArgs a{cached, fresh, static_cast<int>(B), free_pages, static_cast<int>(num_free),
+                            static_cast<int>(num_pages), static_cast<int>(page_size), log2_page(page_size), block_table,
+                            B > 1 ? ld_table : 0, static_cast<int>(width), cu_fresh, kv_len, slots,
+                            static_cast<int>(rows), taken, d->status};
+    cudaError_t e = launch_paged_tables(a, d->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CIDER_OK : cuda_fail(e, "paged-tables launch");
+}
+
+cider_status_t cider_paged_append(const cider_paged_cache_t* cache, const void* k_new, int64_t ld_k, const void* v_new,
+                                  int64_t ld_v, const int32_t* slots, int64_t T, void* stream) {
+    t_last_error[0] = '\0';
+    PagedCache c;
+    size_t span = 0;
+    cider_status_t s = check_cache(cache, &c, &span);
+    if (s != CIDER_OK) return s;
+    if (T < 0 || T > INT32_MAX) return fail(CIDER_ERR_INVALID_ARG, "T = %lld outside [0, 2^31)", (long long)T);
+    const int64_t row = cache->H_kv * cache->D;
+    if ((s = check_ld("ld_k", ld_k, row, T)) != CIDER_OK) return s;
+    if ((s = check_ld("ld_v", ld_v, row, T)) != CIDER_OK) return s;
+    if (cache->k == cache->v) return fail(CIDER_ERR_INVALID_ARG, "the cache's k and v are the same buffer");
+    if (T == 0) return CIDER_OK;
+    if (!k_new || !v_new || !slots) return fail(CIDER_ERR_INVALID_ARG, "NULL pointer");
+    if (!aligned16(k_new) || !aligned16(v_new)) return fail(CIDER_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(slots) & 3u) return fail(CIDER_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+    const Range rk = rng(cache->k, span), rv = rng(cache->v, span);
+    for (const Range& r : {rng(k_new, row_span(T, ld_k, row)), rng(v_new, row_span(T, ld_v, row)),
+                           rng(slots, static_cast<size_t>(T) * 4)})
+        if (overlap(r, rk) || overlap(r, rv)) return fail(CIDER_ERR_INVALID_ARG, "an input overlaps the cache");
+    DeviceInfo* d = nullptr;
+    if ((s = device_info(&d)) != CIDER_OK) return s;
+    cudaError_t e = launch_paged_append(c, k_new, T > 1 ? ld_k : row, v_new, T > 1 ? ld_v : row, slots, static_cast<int>(T),
+                                        d->num_sms, d->status, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CIDER_OK : cuda_fail(e, "paged-append launch");
+}
+
+size_t cider_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t H_q, int64_t H_kv, int64_t D, int64_t max_fresh) {
+    if (check_paged_attn(T, B, H_q, H_kv, D, max_fresh) != CIDER_OK) return 0;
+    DeviceInfo* d = nullptr;
+    if (device_info(&d) != CIDER_OK) return 0;
+    return paged_rows16_bytes(static_cast<int>(D), d->num_sms);
+}
+
+cider_status_t cider_paged_attention(const cider_paged_cache_t* cache, const void* q, int64_t ld_q, int64_t T, int64_t H_q,
+                                     const int32_t* cu_fresh, const int32_t* kv_len, int64_t B,
+                                     const int32_t* block_table, int64_t ld_table, int64_t width, int64_t max_fresh,
+                                     int64_t window, int64_t sinks, float scale, void* out, int64_t ld_out,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+    t_last_error[0] = '\0';
+    PagedCache c;
+    size_t span = 0;
+    cider_status_t s = check_cache(cache, &c, &span);
+    if (s != CIDER_OK) return s;
+    if ((s = check_paged_attn(T, B, H_q, cache->H_kv, cache->D, max_fresh)) != CIDER_OK) return s;
+    const int64_t row = H_q * cache->D;
+    if ((s = check_ld("ld_q", ld_q, row, T)) != CIDER_OK) return s;
+    if ((s = check_ld("ld_out", ld_out, row, T)) != CIDER_OK) return s;
+    if (width < 1 || width > kMaxLen / cache->page_size || (B > 1 && ld_table < width) || (B > 1 && ld_table > kMaxStride))
+        return fail(CIDER_ERR_INVALID_ARG, "width = %lld, ld_table = %lld: 1 <= width <= ld_table, width * page_size <= 2^30",
+                    (long long)width, (long long)ld_table);
+    if (window < 0 || window >= kMaxLen || sinks < 0 || sinks >= kMaxLen)
+        return fail(CIDER_ERR_INVALID_ARG, "window = %lld and sinks = %lld must lie in [0, 2^30)", (long long)window, (long long)sinks);
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(CIDER_ERR_INVALID_ARG, "scale = %g must be finite and > 0", scale);
+    if (T == 0) return CIDER_OK;
+    if (!q || !out || !cu_fresh || !kv_len || !block_table || !workspace) return fail(CIDER_ERR_INVALID_ARG, "NULL pointer");
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
+        return fail(CIDER_ERR_INVALID_ARG, "q, out and workspace must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(cu_fresh) | reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(block_table)) & 3u)
+        return fail(CIDER_ERR_INVALID_ARG, "cu_fresh, kv_len and block_table must be 4-byte aligned");
+    DeviceInfo* d = nullptr;
+    if ((s = device_info(&d)) != CIDER_OK) return s;
+    const size_t need = cider_paged_attention_workspace_bytes(T, B, H_q, cache->H_kv, cache->D, max_fresh);
+    if (workspace_bytes < need)
+        return fail(CIDER_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);
+    const Range ro = rng(out, row_span(T, ld_out, row)), rw = rng(workspace, need);
+    for (const Range& r : {rng(q, row_span(T, ld_q, row)), rng(cache->k, span), rng(cache->v, span),
+                           rng(cu_fresh, static_cast<size_t>(B + 1) * 4), rng(kv_len, static_cast<size_t>(B) * 4),
+                           rng(block_table, (static_cast<size_t>(B - 1) * (B > 1 ? ld_table : 0) + width) * 4)})
+        if (overlap(ro, r) || overlap(rw, r)) return fail(CIDER_ERR_INVALID_ARG, "out or the workspace overlaps an input");
+    if (overlap(ro, rw)) return fail(CIDER_ERR_INVALID_ARG, "out overlaps the workspace");
+    PagedAttnArgs a{};
+    a.c = c;
+    a.q = q;
+    a.ld_q = T > 1 ? ld_q : row;
+    a.T = static_cast<int>(T);
+    a.H_q = static_cast<int>(H_q);
+    a.G = static_cast<int>(H_q / cache->H_kv);
+    a.cu = cu_fresh;
+    a.kv_len = kv_len;
+    a.B = static_cast<int>(B);
+    a.table = block_table;
+    a.ld_table = B > 1 ? ld_table : 0;
+    a.width = static_cast<int>(width);
+    a.window = static_cast<int>(window);
+    a.sinks = static_cast<int>(sinks);
+    a.qscale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.out = out;
+    a.ld_out = T > 1 ? ld_out : row;
+    a.part = static_cast<float*>(workspace);
+    a.status = d->status;
+    cudaError_t e = launch_paged_rows16(a, d->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CIDER_OK : cuda_fail(e, "paged-attention launch");
+}
+
+cider_status_t cider_test_set_paged_kernel(int kernel) {
+    t_last_error[0] = '\0';
+    if (kernel < 0 || kernel > 2) return fail(CIDER_ERR_INVALID_ARG, "kernel %d outside [0, 2]", kernel);
+    g_paged_kernel.store(kernel);
+    return CIDER_OK;
 }
 
 cider_status_t cider_test_gemm_i32(const int8_t* q, const int8_t* w, int64_t M, int64_t N, int64_t K,

@@ -12,6 +12,7 @@ namespace cider {
 
 // Device status word bits (read back by cider_device_status()).
 constexpr unsigned kStatusTimeout = 1u;
+constexpr unsigned kStatusIndex = 2u;  // a length, page number or slot in device memory outside its range
 
 enum : int {
     kModePC = 0,    // per-channel dequant epilogue
