@@ -18,7 +18,9 @@ that of one to fp32, N keys seen and D dims, in the order of the arithmetic:
             multiplies the sums by a factor of error w + e: R (w + e),
             R = N / 16 + 8 (the joins of warps and of pieces)
   sums      O and l add N terms in fp32, rounded toward zero at worst: 2 N e each
-  P         rounded to 16 bits before the product: u
+  P         rounded to 16 bits before the product: u; in fp16, whose weights are
+            made as up to 2^7 and more, those below 2^-14 by half of the smallest
+            subnormal, 2^-25 / 2^7 against the largest weight: N 2^-32 max |v|
   result    O / l: the weight's, rescales' and sums' errors count twice (in O
             and in l), u of P once, each against A = sum_j p_j |v_j|; the
             division and its product 3 e; then one rounding: u |out|, or half of
@@ -121,6 +123,8 @@ def check(batch, out, ref=None, roundings_only=False):
         w = 2 * batch.D * E * S + 6 * E * S + 4 * E
         rel = 2 * (w + (n / 16 + 8) * (w + E) + 2 * n * E) + u + 4 * E
         tol = rel * mag * (1 + u) + u * np.abs(want) + tiny
+        if batch.dt == "f16":
+            tol = tol + n * 2.0 ** -32 * batch.v[batch.v.isfinite()].abs().max().item()
     tol = tol + (n + 2) * 2.0 ** -53 * mag
     err = np.abs(got - want)
     bad = live[:, None, None] & ~(err <= tol) & ~(np.isnan(want) & np.isnan(got)) & ~(want == got)

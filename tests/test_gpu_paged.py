@@ -12,7 +12,7 @@ from oracle import paged
 from tests.paged_cases import Batch, check
 
 pytestmark = pytest.mark.gpu
-KERNELS = [0, 1]
+KERNELS = [0, 1, 2]
 
 
 @pytest.fixture(scope="module", autouse=True)

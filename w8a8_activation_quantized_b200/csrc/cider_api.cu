@@ -809,6 +809,14 @@ cider_status_t check_cache(const cider_paged_cache_t* c, PagedCache* out, size_t
     return CIDER_OK;
 }
 
+// Whether a call runs on the tensor-core tiles: when a request may bring more
+// rows than one 16-row tile holds.
+bool paged_on_tc(int64_t G, int64_t max_fresh, int64_t T) {
+    const int forced = g_paged_kernel.load();
+    if (forced == 1 || !paged_tc_applies(static_cast<int>(G))) return false;
+    return forced == 2 || std::min(max_fresh, T) * G > 16;
+}
+
 cider_status_t check_paged_attn(int64_t T, int64_t B, int64_t H_q, int64_t H_kv, int64_t D, int64_t max_fresh) {
     if (D != 64 && D != 128) return fail(CIDER_ERR_INVALID_ARG, "D = %lld must be 64 or 128", (long long)D);
     if (H_kv < 1 || H_kv > 65535 || H_q < 1 || H_q > 65535 || H_q % H_kv)
@@ -891,6 +899,8 @@ size_t cider_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t H_q, 
     if (check_paged_attn(T, B, H_q, H_kv, D, max_fresh) != CIDER_OK) return 0;
     DeviceInfo* d = nullptr;
     if (device_info(&d) != CIDER_OK) return 0;
+    const int G = static_cast<int>(H_q / H_kv);
+    if (paged_on_tc(G, max_fresh, T)) return paged_tc_bytes(T, B, G, static_cast<int>(D), d->num_sms);
     return paged_rows16_bytes(static_cast<int>(D), d->num_sms);
 }
 
@@ -951,7 +961,8 @@ cider_status_t cider_paged_attention(const cider_paged_cache_t* cache, const voi
     a.ld_out = T > 1 ? ld_out : row;
     a.part = static_cast<float*>(workspace);
     a.status = d->status;
-    cudaError_t e = launch_paged_rows16(a, d->num_sms, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = paged_on_tc(a.G, max_fresh, T) ? launch_paged_tc(a, d->num_sms, st) : launch_paged_rows16(a, d->num_sms, st);
     return e == cudaSuccess ? CIDER_OK : cuda_fail(e, "paged-attention launch");
 }
 

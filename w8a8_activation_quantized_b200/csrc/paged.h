@@ -65,4 +65,10 @@ cudaError_t launch_paged_append(const PagedCache& c, const void* k_new, int64_t 
 size_t paged_rows16_bytes(int D, int num_sms);
 cudaError_t launch_paged_rows16(PagedAttnArgs a, int num_sms, cudaStream_t st);
 
+// Tensor-core tiles: whether they take a group of G heads per KV head, their
+// workspace, and the launches (work list, tiles, join).
+bool paged_tc_applies(int G);
+size_t paged_tc_bytes(int64_t T, int64_t B, int G, int D, int num_sms);
+cudaError_t launch_paged_tc(const PagedAttnArgs& a, int num_sms, cudaStream_t st);
+
 }  // namespace cider

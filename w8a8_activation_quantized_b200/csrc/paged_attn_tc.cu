@@ -1,0 +1,987 @@
+// paged_attn_tc.cu -- attention of chunks of new tokens over a paged key/value
+// cache on the tensor cores (tcgen05): what paged_attn.cu computes, for
+// requests that bring more rows than one of its tiles holds.
+//
+//   out = sum_j p_j V[j] / sum_j p_j,   p_j = 2^((s_j - m) scale log2 e)
+//
+// A unit of work is up to 256 rows -- two tiles of 128 / G tokens with their G
+// query heads of one KV head -- against a run of 128-key blocks.  One CTA per
+// SM works through its units:
+//  * warp 0 copies (TMA, 128-byte swizzle) the unit's queries and, block by
+//    block, K and V through a ring of kStages 128-key tiles.  A tile is
+//    gathered from its pages, one box of 64 dims x page_size keys per page and
+//    half, the page numbers read one block ahead.  Pages that no query of the
+//    unit sees are not read: their boxes lie outside the tensor map, which
+//    fills them with zeros.
+//  * one thread of warp 1 issues the products.  Per block and tile t:
+//    O_t += P_t V, then S_t = Q_t K^T of the next block, so that each tile's
+//    softmax runs while the tensor pipe works for the other tile.
+//  * two warpgroups do the softmax, one per tile, one thread per row (no
+//    shuffles): S_t from tensor memory, mask, maximum, weights, sum; P_t goes
+//    back in 16 bits over S_t's first 64 columns and is the product's operand
+//    from there.  O_t stays in tensor memory (S 2 x 128, O 2 x D columns).
+//    The maximum is a reference, not the exact one: it moves (and O_t and the
+//    sum are rescaled) only when a row's maximum has grown by a factor of 2^8
+//    or more, which after the first blocks hardly happens.  Weights then reach
+//    2^8 times 2^kOff at most, and the fp32 sums lose nothing by it.
+//  * Rows of V that no query of the unit sees (behind the request's end, or in
+//    front of the window) are zeroed in shared memory before the product that
+//    would multiply them by zero weights: what an unused slot holds may be NaN.
+//    If a row of V that some query of the unit must not see, while others do,
+//    holds NaN or an infinity, the tile's rows are computed again one by one
+//    (redo_row), so that it reaches only the queries that see it.
+//
+// What bounds it: per 128 x 128 block of scores the two products take 1024
+// cycles of the tensor pipe at D = 128 (8192 fp16 operations per cycle and SM),
+// and the 16384 exponentials 1024 cycles of the special-function units (16 per
+// cycle and SM).
+//
+// The work list is made by a one-CTA kernel that reads the lengths on the
+// device: it lists the units longest first (each CTA takes them in snake
+// order, so the SMs finish together) and, when they are too few for the SMs,
+// cuts their key blocks into pieces whose fp32 results another kernel joins.
+// Every wait is bounded (mbar_wait).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+#include "gemm_common.cuh"
+#include "paged_common.cuh"
+
+namespace cider {
+namespace {
+
+constexpr int kKeys = 128;                     // keys per block
+constexpr int kTcThreads = 384;                // warps 0-3: TMA, MMA, two idle; then a softmax warpgroup per tile
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxPieces = 32;
+constexpr int kSlotsPerSm = 2;                 // places for pieces' partial results, per SM
+constexpr float kLazy = 8.0f;                  // log2 of the growth of a maximum that is put off
+
+// One unit: tokens [token0, token0 + ntok) of q's rows, the first at position
+// pmin, against blocks [vb0, vb0 + nblk) of its span; slot -1: the whole span.
+struct __align__(16) TcUnit {
+    int b, token0, ntok, pmin, vb0, nblk, slot, pad;
+};
+struct __align__(16) TcJoin {
+    int token0, ntok, slot, pieces;  // slot of (piece, head) = slot + piece * H_kv + head
+};
+struct TcPlan {
+    int units, joins;  // records, each for H_kv heads
+};
+
+struct TcArgs {
+    PagedAttnArgs p;
+    int tok;              // tokens per 128-row tile: 128 / G
+    int boxes;            // pages per block (at least 1)
+    int box_keys;         // keys per box: min(page_size, 128)
+    int d_tok, d_head;    // which of the map's outer dimensions (1..3) is the token, the head; the page is the third
+    int grid;
+    TcPlan* plan;
+    TcUnit* units;
+    TcJoin* joins;
+    float* part;          // [slot][256][D], then [slot][256] maximum and sum
+    int slots;
+};
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x, PTX ex2.approx (relative error near 2^-22)
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Weights are made as 2^(x + kOff).  fp16: 2^7, with the lazy maximum up to
+// 2^15 < 65504, so weights down to 2^-21 of the reference keep all 11 bits;
+// bf16 has the range of fp32.  The factor cancels in O / l.
+template <typename T>
+constexpr float kOff = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+
+// ---- the work list ------------------------------------------------------------
+
+// Blocks that the queries [pmin, pmin + ntok) read.
+__device__ __forceinline__ int span_blocks(const PagedAttnArgs& a, int pmin, int ntok) {
+    PagedSpan<kKeys> s;
+    s.set(pmin, pmin + ntok - 1, a.window, a.sinks);
+    return s.blocks;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
+    extern __shared__ int32_t pre[];  // [B + 1] tiles before each request
+    __shared__ int64_t s_warp[kPlanThreads / 32];
+    __shared__ int s_hist[1024];
+    __shared__ float s_cost[kMaxPieces];
+    __shared__ int s_max, s_chunk, s_slot, s_joins;
+    __shared__ unsigned long long s_work;
+    const PagedAttnArgs& a = t.p;
+    const int per_unit = 2 * t.tok;
+    pdl_wait();
+    pdl_trigger();
+    s_hist[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        s_max = s_slot = s_joins = 0;
+        s_work = 0;
+    }
+    const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    int sum = 0;
+    bool any_bad = false;
+    for (int b = b0; b < b1; ++b) {
+        bool bad;
+        const PagedRequest r = paged_request(a, b, &bad);
+        any_bad |= bad;
+        pre[b] = sum;
+        sum += (r.n + per_unit - 1) / per_unit;
+    }
+    if (any_bad) atomicOr(a.status, kStatusIndex);
+    int64_t total;
+    const int base = static_cast<int>(block_prefix<kPlanThreads>(sum, s_warp, &total));
+    for (int b = b0; b < b1; ++b) pre[b] += base;
+    if (threadIdx.x == 0) pre[a.B] = static_cast<int>(total);
+    __syncthreads();
+    const int tiles = static_cast<int>(total);
+    auto unit = [&](int i) {
+        TcUnit u;
+        u.b = find_request(pre, a.B, i);
+        bool bad;
+        const PagedRequest r = paged_request(a, u.b, &bad);
+        const int first = (i - pre[u.b]) * per_unit;
+        u.token0 = r.start + first;
+        u.ntok = min(per_unit, r.n - first);
+        u.pmin = r.L - r.n + first;
+        u.vb0 = 0;
+        u.nblk = span_blocks(a, u.pmin, u.ntok);
+        u.slot = -1;
+        u.pad = 0;
+        return u;
+    };
+    int mx = 0;
+    unsigned long long work = 0;
+    for (int i = threadIdx.x; i < tiles; i += kPlanThreads) {
+        const int n = unit(i).nblk;
+        mx = max(mx, n);
+        work += n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        work += __shfl_xor_sync(0xffffffffu, work, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        atomicMax(&s_max, mx);
+        atomicAdd(&s_work, work);
+    }
+    __syncthreads();
+    mx = s_max;
+    // How long a piece may be.  Units enough for two rounds of the SMs: whole
+    // spans.  Fewer: warp w tries the longest span cut into w + 1; the cost of a
+    // cut is the longest piece, or the rounds' average, in blocks, plus about
+    // two blocks per unit to start and end it and four for the join.
+    const int64_t whole_units = static_cast<int64_t>(tiles) * a.c.H_kv;
+    if (whole_units < 2 * t.grid && mx > 1) {
+        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int chunk = (mx + w) / (w + 1);
+        int pieces = 0;
+        for (int i = lane; i < tiles; i += 32) pieces += max(1, (unit(i).nblk + chunk - 1) / chunk);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
+        if (lane == 0) {
+            const int64_t units = static_cast<int64_t>(pieces) * a.c.H_kv;
+            const int64_t rounds = (units + t.grid - 1) / t.grid;
+            const float avg = static_cast<float>(s_work) * a.c.H_kv / units;
+            float cost = fmaxf(chunk, rounds * avg) + 2.0f * rounds + (w > 0 ? 4.0f : 0.0f);
+            if (w > 0 && units > t.slots) cost = FLT_MAX;  // no place for the partial results
+            s_cost[w] = cost;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int best = 0;
+            for (int i = 1; i < kMaxPieces; ++i)
+                if (s_cost[i] < s_cost[best]) best = i;
+            s_chunk = (mx + best) / (best + 1);
+        }
+    } else if (threadIdx.x == 0) {
+        s_chunk = max(mx, 1);
+    }
+    __syncthreads();
+    const int chunk = s_chunk;
+    // longest first: count the pieces per length class, then place them
+    const float scale = 1023.0f / max(1, min(mx, chunk));
+    auto bin = [&](int n) { return 1023 - min(1023, static_cast<int>(n * scale)); };
+    auto piece_len = [&](int n, int k, int q) {  // [q n / k, (q + 1) n / k)
+        return static_cast<int>(static_cast<int64_t>(n) * (q + 1) / k - static_cast<int64_t>(n) * q / k);
+    };
+    for (int i = threadIdx.x; i < tiles; i += kPlanThreads) {
+        const int n = unit(i).nblk, k = max(1, (n + chunk - 1) / chunk);
+        for (int q = 0; q < k; ++q) atomicAdd(&s_hist[bin(piece_len(n, k, q))], 1);
+    }
+    __syncthreads();
+    int64_t all;
+    const int64_t at = block_prefix<kPlanThreads>(s_hist[threadIdx.x], s_warp, &all);
+    s_hist[threadIdx.x] = static_cast<int>(at);
+    __syncthreads();
+    for (int i = threadIdx.x; i < tiles; i += kPlanThreads) {
+        TcUnit u = unit(i);
+        const int n = u.nblk, k = max(1, (n + chunk - 1) / chunk);
+        int slot = -1;
+        if (k > 1) {
+            slot = atomicAdd(&s_slot, k * a.c.H_kv);
+            t.joins[atomicAdd(&s_joins, 1)] = TcJoin{u.token0, u.ntok, slot, k};
+        }
+        for (int q = 0; q < k; ++q) {
+            u.vb0 = static_cast<int>(static_cast<int64_t>(n) * q / k);
+            u.nblk = piece_len(n, k, q);
+            u.slot = k > 1 ? slot + q * a.c.H_kv : -1;
+            t.units[atomicAdd(&s_hist[bin(u.nblk)], 1)] = u;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) *t.plan = TcPlan{static_cast<int>(all), s_joins};
+}
+
+// ---- tensor-core pieces ---------------------------------------------------------
+
+// Operand stored with rows of 128 bytes along MN (64 16-bit elements, 128-byte
+// swizzle) and 8-row groups along K 1024 bytes apart; `lbo` bytes between
+// 64-element atoms along MN.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;  // version
+    d |= static_cast<uint64_t>(2u) << 61;  // SWIZZLE_128B
+    return d;
+}
+
+// kind::f16 instruction descriptor: D = F32, A = B = fp16 (bf = 0) or bf16 (bf
+// = 1); b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, int bf, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(bf) << 7) | (static_cast<uint32_t>(bf) << 10) |
+           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A from tensor memory: row = lane, two 16-bit values of K per column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// Barrier of the 128 threads of softmax warpgroup wg; true if any passes x.
+__device__ __forceinline__ bool group_or(int wg, bool x) {
+    uint32_t y;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(y)
+        : "r"(static_cast<uint32_t>(x)), "r"(1 + wg)
+        : "memory");
+    return y != 0;
+}
+
+template <int D>
+__device__ __forceinline__ float* part_row(const TcArgs& t, int slot, int row) {
+    return t.part + (static_cast<int64_t>(slot) * 256 + row) * D;
+}
+template <int D>
+__device__ __forceinline__ float2* part_ml(const TcArgs& t, int slot, int row) {
+    return reinterpret_cast<float2*>(t.part + static_cast<int64_t>(t.slots) * 256 * D) + static_cast<int64_t>(slot) * 256 + row;
+}
+
+// One row of a unit on the CUDA cores, key by key: only the keys that this row
+// sees are touched.  Rare (see the top of the file), so it is simple: a first
+// pass over the keys for the maximum and the sum, then one per 32 dims.
+template <typename T, int D>
+__device__ __noinline__ void redo_row(const TcArgs& t, const TcUnit& u, int head, const T* q, int pos, T* out,
+                                      float* part, float2* ml) {
+    const PagedAttnArgs& a = t.p;
+    PagedSpan<kKeys> span;
+    span.set(u.pmin, u.pmin + u.ntok - 1, a.window, a.sinks);
+    const int32_t* table = a.table + u.b * a.ld_table;
+    const T* kh = reinterpret_cast<const T*>(a.c.k) + head * a.c.sh;
+    const T* vh = reinterpret_cast<const T*>(a.c.v) + head * a.c.sh;
+    float m = -INFINITY, l = 0.0f;
+    for (int pass = 0; pass <= D / 32; ++pass) {
+        float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        for (int vb = u.vb0; vb < u.vb0 + u.nblk; ++vb) {
+            const int key0 = span.block(vb) * kKeys;
+            for (int key = key0; key < key0 + kKeys; ++key) {
+                if (!paged_sees(key, pos, a.window, a.sinks)) continue;
+                const int page = __ldg(table + (key >> a.c.ps_log2));
+                if (page < 0 || page >= a.c.num_pages) continue;
+                const int64_t off = page * a.c.sp + (key & (a.c.page_size - 1)) * a.c.st;
+                float s = 0.0f;
+                for (int d = 0; d < D; d += 8) {
+                    float x[8], y[8];
+                    unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(q + d)), x);
+                    unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(kh + off + d)), y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+                }
+                if (pass == 0) {
+                    const float mn = fmaxf(fmaxf(m, s), -FLT_MAX);
+                    const float f = mn == m ? 1.0f : ex2((m - mn) * a.qscale);
+                    l = l * f + ex2(fmaf(s, a.qscale, kOff<T> - mn * a.qscale));
+                    m = mn;
+                } else {
+                    const float p = ex2(fmaf(s, a.qscale, kOff<T> - m * a.qscale));
+                    const T* v = vh + off + (pass - 1) * 32;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = fmaf(p, to_f32<T>(v[i]), o[i]);
+                }
+            }
+        }
+        if (pass == 0) {
+            if (ml) *ml = make_float2(m, l);
+            continue;
+        }
+        const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (part)
+                part[(pass - 1) * 32 + i] = o[i];
+            else
+                out[(pass - 1) * 32 + i] = from_f32<T>(o[i] * inv);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ bool nonfinite8(const uint4& v) {
+    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (w[i] & e) == e || (w[i] & (e << 16)) == (e << 16);
+    return bad;
+}
+
+template <int D>
+constexpr int kTileBytes = kKeys * D * 2;  // one K or V tile; one tile of queries is the same
+template <int D>
+constexpr int kStages = D == 128 ? 5 : 8;
+constexpr int kTmemCols = 512;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constant__ CUtensorMap tmQ,
+                                                            const __grid_constant__ CUtensorMap tmK,
+                                                            const __grid_constant__ CUtensorMap tmV, const TcArgs t) {
+    constexpr int BF = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    constexpr int ST = kStages<D>;
+    constexpr int TB = kTileBytes<D>;
+    constexpr int AB = kKeys * 128;  // one 64-dim atom of a tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sQ = smem;               // two tiles of queries
+    uint8_t* sRing = smem + 2 * TB;   // ST tiles of keys or values: K, V, K, V, ...
+    __shared__ uint64_t qfull, qempty, full[ST], empty[ST], sfull[2], pfull[2], odone[2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int s_abort;
+    volatile int* abort_flag = &s_abort;
+    const PagedAttnArgs& a = t.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        mbar_init(&qfull, 1);
+        mbar_init(&qempty, 1);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 128);
+            mbar_init(&odone[i], 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 1) tmem_alloc(&tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+    unsigned* status = a.status;
+    const int nunits = t.plan->units * a.c.H_kv;
+    const int rounds = (nunits + t.grid - 1) / t.grid;
+    // round r of this CTA: snake order over the list, which is sorted
+    auto unit_index = [&](int r) {
+        const int i = static_cast<int>(blockIdx.x);
+        return r * t.grid + ((r & 1) ? t.grid - 1 - i : i);
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            // ------------------------------ TMA producer ------------------------------
+            int tile = 0, nq = 0;  // tiles of the ring, and queries, so far
+            bool ok = true;
+            for (int r = 0; r < rounds && ok; ++r) {
+                const int ui = unit_index(r);
+                if (ui >= nunits) continue;
+                const TcUnit u = t.units[ui / a.c.H_kv];
+                const int head = ui % a.c.H_kv;
+                if (u.nblk == 0) continue;
+                PagedSpan<kKeys> span;
+                span.set(u.pmin, u.pmin + u.ntok - 1, a.window, a.sinks);
+                const int32_t* table = a.table + u.b * a.ld_table;
+                // page of this lane's box of block vb; num_pages (outside the map:
+                // zeros) where no query sees any of its keys, or the page is bad
+                auto page_of = [&](int vb) {
+                    int page = a.c.num_pages;
+                    if (lane < t.boxes && vb < u.vb0 + u.nblk) {
+                        const int key0 = span.block(vb) * kKeys + lane * t.box_keys;
+                        const bool used = key0 <= span.pmax && (a.window <= 0 || key0 + t.box_keys - 1 > span.pmin - a.window || key0 < a.sinks);
+                        if (used) {
+                            const int p = __ldg(table + (key0 >> a.c.ps_log2));
+                            if (p >= 0 && p < a.c.num_pages)
+                                page = p;
+                            else
+                                atomicOr(status, kStatusIndex);
+                        }
+                    }
+                    return page;
+                };
+                int next = page_of(u.vb0);
+                for (int i = 0; i < u.nblk && ok; ++i) {
+                    const int page = next;
+                    next = page_of(u.vb0 + i + 1);
+                    const int in_page = (span.block(u.vb0 + i) * kKeys) & (a.c.page_size - 1);  // pages of 256: 0 or 128
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++tile) {
+                        const int s = tile % ST;
+                        ok = ok && mbar_wait(&empty[s], ((tile / ST) & 1) ^ 1, status, abort_flag);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&full[s], TB);
+                        __syncwarp();
+                        // one box per page and 64-dim half, a lane each
+                        const int box = lane % t.boxes, half = lane / t.boxes;
+                        const int pg = __shfl_sync(0xffffffffu, page, box);
+                        if (half < D / 64) {
+                            const CUtensorMap* map = kv ? &tmV : &tmK;
+                            int c[4] = {half * 64, pg, pg, pg};
+#pragma unroll
+                            for (int d = 1; d < 4; ++d) {
+                                if (d == t.d_tok) c[d] = in_page;
+                                if (d == t.d_head) c[d] = head;
+                            }
+                            tma_load_4d(sRing + s * TB + half * AB + box * t.box_keys * 128, map, &full[s], c[0], c[1], c[2], c[3]);
+                        }
+                        __syncwarp();
+                    }
+                    if (i == 0 && ok) {  // the queries, once the last unit's products are done with theirs
+                        ok = mbar_wait(&qempty, (nq & 1) ^ 1, status, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        const int tiles = u.ntok > t.tok ? 2 : 1;
+                        const int bytes = t.tok * a.G * 128;
+                        if (ok && lane == 0) {
+                            mbar_arrive_expect_tx(&qfull, tiles * (D / 64) * bytes);
+                            for (int h = 0; h < tiles; ++h)
+                                for (int d = 0; d < D / 64; ++d)
+                                    tma_load_3d(sQ + h * TB + d * AB, &tmQ, &qfull, d * 64, head * a.G, u.token0 + h * t.tok);
+                        }
+                        __syncwarp();
+                        ++nq;
+                    }
+                }
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------ MMA issuer --------------------------------
+            constexpr uint32_t idesc_s = idesc_16(128, kKeys, BF, 0);
+            constexpr uint32_t idesc_o = idesc_16(128, D, BF, 1);
+            int tile = 0, nq = 0, blk[2] = {0, 0};  // blk: blocks of each tile so far
+            bool ok = true;
+            for (int r = 0; r < rounds && ok; ++r) {
+                const int ui = unit_index(r);
+                if (ui >= nunits) continue;
+                const TcUnit u = t.units[ui / a.c.H_kv];
+                if (u.nblk == 0) continue;
+                const int tiles = u.ntok > t.tok ? 2 : 1;
+                auto scores = [&](int h, int s) {  // S_h = Q_h K^T
+                    const uint32_t a0 = smem_u32(sQ + h * TB), b0 = smem_u32(sRing + s * TB);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * AB + (kk & 3) * 32;
+                        mma_ss(tmem + h * 128, umma_desc_sw128(a0 + off), umma_desc_sw128(b0 + off), idesc_s, kk > 0);
+                    }
+                    umma_commit(&sfull[h]);
+                };
+                {
+                    const int s = tile % ST;
+                    ok = mbar_wait(&full[s], (tile / ST) & 1, status, abort_flag) && mbar_wait(&qfull, nq & 1, status, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int h = 0; h < tiles; ++h) scores(h, s);
+                    umma_commit(&empty[s]);
+                    if (u.nblk == 1) umma_commit(&qempty);
+                    ++tile;
+                }
+                ++nq;
+                for (int i = 0; i < u.nblk && ok; ++i) {
+                    const int sv = tile % ST, vph = (tile / ST) & 1;
+                    const int sk = (tile + 1) % ST, kph = ((tile + 1) / ST) & 1;
+                    const bool more = i + 1 < u.nblk;
+                    for (int h = 0; h < tiles && ok; ++h) {
+                        if (h == 0) ok = mbar_wait(&full[sv], vph, status, abort_flag);
+                        ok = ok && mbar_wait(&pfull[h], blk[h] & 1, status, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t v0 = smem_u32(sRing + sv * TB);
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of each atom of V
+                            mma_ts(tmem + 256 + h * D, tmem + h * 128 + kk * 8, desc_mn(v0 + kk * 2048, AB), idesc_o,
+                                   i > 0 || kk > 0);
+                        umma_commit(&odone[h]);
+                        ++blk[h];
+                        if (more) {
+                            if (h == 0) {
+                                ok = mbar_wait(&full[sk], kph, status, abort_flag);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+                            scores(h, sk);
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit(&empty[sv]);
+                    if (more) {
+                        umma_commit(&empty[sk]);
+                        if (i + 2 == u.nblk) umma_commit(&qempty);  // the unit's last scores are made
+                    }
+                    tile += more ? 2 : 1;
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ softmax and output ----------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int h = (warp - 4) >> 2;  // this warpgroup's tile
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_addr + h * 128, tO = tmem + lane_addr + 256 + h * D;
+        int nb = 0;    // blocks of this tile so far
+        int vtile = 0; // the ring's index of the unit's first K tile
+        bool ok = true;
+        for (int r = 0; r < rounds && ok; ++r) {
+            const int ui = unit_index(r);
+            if (ui >= nunits) continue;
+            const TcUnit u = t.units[ui / a.c.H_kv];
+            const int head = ui % a.c.H_kv;
+            const int tok0 = h * t.tok, ntok = min(t.tok, u.ntok - tok0);  // this tile's tokens
+            if (ntok <= 0) {
+                vtile += 2 * u.nblk;
+                continue;
+            }
+            PagedSpan<kKeys> span;
+            span.set(u.pmin, u.pmin + u.ntok - 1, a.window, a.sinks);
+            const int pmin = u.pmin + tok0, pmax = pmin + ntok - 1;
+            const int tok = row / a.G;
+            const int pos = pmin + tok;
+            const bool live = tok < ntok && row < t.tok * a.G;
+            const int32_t* table = a.table + u.b * a.ld_table;
+            // does any block that some query of the unit sees lack its page?
+            bool bad = false;
+            for (int e = row; e < u.nblk * t.boxes; e += 128) {
+                const int key0 = span.block(u.vb0 + e / t.boxes) * kKeys + (e % t.boxes) * t.box_keys;
+                if (key0 <= span.pmax && (a.window <= 0 || key0 + t.box_keys - 1 > span.pmin - a.window || key0 < a.sinks)) {
+                    const int p = __ldg(table + (key0 >> a.c.ps_log2));
+                    bad |= p < 0 || p >= a.c.num_pages;
+                }
+            }
+            bad = group_or(h, bad);
+            float m = -INFINITY, l = 0.0f;
+            bool poison = false;
+            for (int i = 0; i < u.nblk; ++i, ++nb) {
+                const int key0 = span.block(u.vb0 + i) * kKeys;
+                ok = mbar_wait(&sfull[h], nb & 1, status, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t sr[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, sr[c]);
+                tmem_ld_wait();
+                float low = -FLT_MAX;  // a row that has seen a key has a finite maximum
+                const bool whole = !bad && key0 + kKeys - 1 <= pmin &&
+                                   (a.window <= 0 || key0 > pmax - a.window || key0 + kKeys <= a.sinks);
+                if (!whole) {
+                    uint32_t pages = 0xff;  // bit per box: has a page
+                    if (bad) {
+                        pages = 0;
+                        for (int e = 0; e < t.boxes; ++e) {
+                            const int k0 = key0 + e * t.box_keys;
+                            if (k0 <= span.pmax && (a.window <= 0 || k0 + t.box_keys - 1 > span.pmin - a.window || k0 < a.sinks)) {
+                                const int p = __ldg(table + (k0 >> a.c.ps_log2));
+                                if (p >= 0 && p < a.c.num_pages) pages |= 1u << e;
+                            }
+                        }
+                    }
+                    const int last = pos - key0;                                                   // seen: c <= last
+                    const int first = a.window > 0 ? max(pos - a.window, -1) - key0 : -1;          // and c > first
+                    const int sink = a.window > 0 ? max(min(a.sinks - key0, kKeys), 0) : 0;        // or c < sink
+                    const int box_log2 = 31 - __clz(t.box_keys);
+                    bool any = false;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int x = c * 32 + e;
+                            const bool see = x <= last && (x > first || x < sink) && ((pages >> (x >> box_log2)) & 1u);
+                            if (!see) sr[c][e] = 0xff800000u;  // -inf
+                            any |= see;
+                        }
+                    if (!any) low = -INFINITY;
+                    // V: zero the rows that no query of the unit sees; look for
+                    // NaN and infinities in the others
+                    const int vt = vtile + 2 * i + 1, s = vt % ST;
+                    ok = mbar_wait(&full[s], (vt / ST) & 1, status, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    for (int e = row; e < kKeys * (D / 8); e += 128) {
+                        const int key = key0 + ((e >> 3) & (kKeys - 1));
+                        uint4* v = reinterpret_cast<uint4*>(sRing + s * TB) + e;
+                        const bool used = key <= span.pmax && (a.window <= 0 || key > span.pmin - a.window || key < a.sinks);
+                        if (!used)
+                            *v = make_uint4(0, 0, 0, 0);
+                        else
+                            poison |= nonfinite8<T>(*v);
+                    }
+                    fence_async_smem();
+                }
+                // maximum of the row (the reference moves only if it grew by 2^kLazy)
+                float mx = low;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(sr[c][e]));
+                const bool grow = (mx - m) * a.qscale > kLazy;  // from -inf: always
+                float f = 1.0f;
+                if (grow) {
+                    f = ex2((m - mx) * a.qscale);
+                    m = mx;
+                    l *= f;
+                }
+                if (i > 0 && __any_sync(0xffffffffu, grow)) {
+                    ok = mbar_wait(&odone[h], (nb - 1) & 1, status, abort_flag);  // O is complete up to the last block
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(tO + c * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st_32x32b_x32(tO + c * 32, o);
+                    }
+                    tmem_st_wait();
+                }
+                const float ms = kOff<T> - (m == -INFINITY ? 0.0f : m) * a.qscale;  // nothing seen yet: all weights 0
+                const uint64_t qs2 = pack_f32x2(a.qscale, a.qscale), ms2 = pack_f32x2(ms, ms);
+                uint64_t l2 = 0;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const uint32_t* s2 = &sr[2 * c + (e >> 4)][(2 * e) & 31];
+                        const uint64_t x = fma_f32x2((static_cast<uint64_t>(s2[1]) << 32) | s2[0], qs2, ms2);
+                        const float p0 = ex2(lo_f32(x)), p1 = ex2(hi_f32(x));
+                        l2 = add_f32x2(l2, pack_f32x2(p0, p1));
+                        p[e] = pack2<T>(p0, p1);
+                    }
+                    tmem_st_32x32b_x32(tS + c * 32, p);
+                }
+                l += lo_f32(l2) + hi_f32(l2);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&pfull[h]);
+            }
+            vtile += 2 * u.nblk;
+            if (u.nblk > 0 && ok) {
+                ok = mbar_wait(&odone[h], (nb - 1) & 1, status, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+            }
+            poison = group_or(h, poison);
+            ok = !group_or(h, !ok);  // the group's warps go on, or end, together
+            if (!ok) break;
+            const int slot = u.slot < 0 ? -1 : u.slot + head;
+            const int64_t q_row = u.token0 + tok0 + tok;
+            const int64_t q_col = static_cast<int64_t>(head * a.G + (row - tok * a.G)) * D;
+            T* out = static_cast<T*>(a.out) + q_row * a.ld_out + q_col;
+            if (poison) {
+                if (live)
+                    redo_row<T, D>(t, u, head, static_cast<const T*>(a.q) + q_row * a.ld_q + q_col, pos, out,
+                                   slot >= 0 ? part_row<D>(t, slot, h * 128 + row) : nullptr,
+                                   slot >= 0 ? part_ml<D>(t, slot, h * 128 + row) : nullptr);
+                continue;
+            }
+            const float inv = m == -INFINITY ? 0.0f : 1.0f / l;  // nothing seen: zeros
+            if (slot >= 0 && live) *part_ml<D>(t, slot, h * 128 + row) = make_float2(m, l);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (u.nblk > 0) {
+                    tmem_ld_32x32b_x32(tO + c * 32, o);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+                if (!live) continue;
+                if (slot >= 0) {
+                    float4* p = reinterpret_cast<float4*>(part_row<D>(t, slot, h * 128 + row) + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        p[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                           __uint_as_float(o[4 * e + 3]));
+                } else {
+                    uint4* p = reinterpret_cast<uint4*>(out + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) v[x] = m == -INFINITY ? 0.0f : __uint_as_float(o[8 * e + x]) * inv;
+                        p[e] = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (s_abort) {  // a wait ran out: give this CTA's copies in flight time to land
+        const unsigned long long t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the pieces of the tiles that were cut, a warp per row:
+// out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_paged_tc_join(const TcArgs t) {
+    pdl_wait();
+    pdl_trigger();
+    const PagedAttnArgs& a = t.p;
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = static_cast<int64_t>(t.plan->joins) * a.c.H_kv * 256;
+    for (int64_t x = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; x < rows; x += gridDim.x * 8) {
+        const int row = static_cast<int>(x & 255);
+        const int64_t y = x >> 8;
+        const int head = static_cast<int>(y % a.c.H_kv);
+        const TcJoin j = t.joins[y / a.c.H_kv];
+        const int tok = (row >> 7) * t.tok + (row & 127) / a.G;
+        if ((row & 127) >= t.tok * a.G || tok >= j.ntok) continue;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < j.pieces) ml = *part_ml<D>(t, j.slot + lane * a.c.H_kv + head, row);
+        float mx = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float f = ml.x == mx ? 1.0f : ex2((ml.x - mx) * a.qscale);
+        float l = ml.y * f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        float o[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
+#pragma unroll 4
+        for (int c = 0; c < j.pieces; ++c) {
+            const float w = __shfl_sync(0xffffffffu, f, c);
+            const float* p = part_row<D>(t, j.slot + c * a.c.H_kv + head, row) + lane * (D / 32);
+            if constexpr (D == 128) {
+                const float4 v = *reinterpret_cast<const float4*>(p);
+                o[0] = fmaf(v.x, w, o[0]);
+                o[1] = fmaf(v.y, w, o[1]);
+                o[2] = fmaf(v.z, w, o[2]);
+                o[3] = fmaf(v.w, w, o[3]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(p);
+                o[0] = fmaf(v.x, w, o[0]);
+                o[1] = fmaf(v.y, w, o[1]);
+            }
+        }
+        const float inv = mx == -INFINITY ? 0.0f : 1.0f / l;
+        T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(j.token0) + tok) * a.ld_out +
+                 static_cast<int64_t>(head * a.G + (row & 127) % a.G) * D + lane * (D / 32);
+#pragma unroll
+        for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack2<T>(o[e] * inv, o[e + 1] * inv);
+    }
+}
+
+// ---- host -------------------------------------------------------------------------
+
+int64_t max_tiles(int64_t T, int64_t B, int tok) { return T / (2 * tok) + B; }
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct TcLayout {
+    size_t units, joins, part, total;
+};
+TcLayout tc_layout(int64_t T, int64_t B, int G, int D, int num_sms) {
+    const int tok = 128 / G;
+    const int64_t slots = static_cast<int64_t>(kSlotsPerSm) * num_sms;
+    TcLayout l;
+    l.units = 256;
+    l.joins = l.units + align256((max_tiles(T, B, tok) + slots) * sizeof(TcUnit));
+    l.part = l.joins + align256(slots * sizeof(TcJoin));
+    l.total = l.part + slots * 256 * (D + 2) * sizeof(float);
+    return l;
+}
+
+template <typename T, int D>
+cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
+    TcArgs t{};
+    t.p = p;
+    t.tok = 128 / p.G;
+    t.box_keys = std::min(p.c.page_size, kKeys);
+    t.boxes = kKeys / t.box_keys;
+    t.grid = num_sms;
+    t.slots = kSlotsPerSm * num_sms;
+    const TcLayout l = tc_layout(p.T, p.B, p.G, D, num_sms);
+    char* ws = reinterpret_cast<char*>(p.part);
+    t.plan = reinterpret_cast<TcPlan*>(ws);
+    t.units = reinterpret_cast<TcUnit*>(ws + l.units);
+    t.joins = reinterpret_cast<TcJoin*>(ws + l.joins);
+    t.part = reinterpret_cast<float*>(ws + l.part);
+
+    // Cache maps: dims {D, then token, head and page by ascending stride}.
+    struct Dim {
+        int64_t n, stride;
+        int id;
+    } dim[3] = {{p.c.page_size, p.c.st, 0}, {p.c.H_kv, p.c.H_kv > 1 ? p.c.sh : 0, 1}, {p.c.num_pages, p.c.num_pages > 1 ? p.c.sp : 0, 2}};
+    std::stable_sort(dim, dim + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D)}, strides[3];
+    cuuint32_t box[4] = {64, 1, 1, 1}, ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        dims[i + 1] = dim[i].n;
+        strides[i] = std::max<int64_t>(dim[i].stride, D) * 2;  // a dimension of one element: any stride
+        if (dim[i].id == 0) {
+            t.d_tok = i + 1;
+            box[i + 1] = t.box_keys;
+        }
+        if (dim[i].id == 1) t.d_head = i + 1;
+    }
+    const auto type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap tmQ, tmK, tmV;
+    if (!encode_tensor_map(&tmK, type, 4, p.c.k, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tensor_map(&tmV, type, 4, p.c.v, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    const cuuint64_t qd[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.H_q), static_cast<cuuint64_t>(p.T)};
+    const cuuint64_t qs[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(p.ld_q) * 2};
+    const cuuint32_t qb[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(t.tok)};
+    if (!encode_tensor_map(&tmQ, type, 3, const_cast<void*>(p.q), qd, qs, qb, ones, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+
+    const int smem = 1024 + (2 + kStages<D>) * kTileBytes<D>;
+    auto kern = k_paged_tc<T, D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_pdl(k_paged_plan, dim3(1), dim3(kPlanThreads), (p.B + 1) * 4, st, t)) != cudaSuccess) return e;
+    if ((e = launch_pdl(kern, dim3(num_sms), dim3(kTcThreads), smem, st, tmQ, tmK, tmV, t)) != cudaSuccess) return e;
+    return launch_pdl(k_paged_tc_join<T, D>, dim3(2 * num_sms), dim3(256), 0, st, t);
+}
+
+}  // namespace
+
+bool paged_tc_applies(int G) { return G <= 128; }
+
+size_t paged_tc_bytes(int64_t T, int64_t B, int G, int D, int num_sms) { return tc_layout(T, B, G, D, num_sms).total; }
+
+cudaError_t launch_paged_tc(const PagedAttnArgs& a, int num_sms, cudaStream_t st) {
+    if (a.c.dt == 1) return a.c.D == 128 ? launch_tc<__nv_bfloat16, 128>(a, num_sms, st) : launch_tc<__nv_bfloat16, 64>(a, num_sms, st);
+    return a.c.D == 128 ? launch_tc<__half, 128>(a, num_sms, st) : launch_tc<__half, 64>(a, num_sms, st);
+}
+
+}  // namespace cider
