@@ -322,6 +322,12 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (std::is_same<T, __half>::value) {
@@ -360,7 +366,7 @@ __device__ __forceinline__ float2* part_ml(const TcArgs& t, int slot, int row) {
 // sees are touched.  Rare (see the top of the file), so it is simple: a first
 // pass over the keys for the maximum and the sum, then one per 32 dims.
 template <typename T, int D>
-__device__ __noinline__ void redo_row(const TcArgs& t, const TcUnit& u, int head, const T* q, int pos, T* out,
+__device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const T* q, int pos, T* out,
                                       float* part, float2* ml) {
     const PagedAttnArgs& a = t.p;
     PagedSpan<kKeys> span;
@@ -435,7 +441,8 @@ constexpr int kTmemCols = 512;
 template <typename T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constant__ CUtensorMap tmQ,
                                                             const __grid_constant__ CUtensorMap tmK,
-                                                            const __grid_constant__ CUtensorMap tmV, const TcArgs t) {
+                                                            const __grid_constant__ CUtensorMap tmV,
+                                                            const __grid_constant__ TcArgs t) {
     constexpr int BF = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
     constexpr int ST = kStages<D>;
     constexpr int TB = kTileBytes<D>;
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;               // two tiles of queries
     uint8_t* sRing = smem + 2 * TB;   // ST tiles of keys or values: K, V, K, V, ...
-    __shared__ uint64_t qfull, qempty, full[ST], empty[ST], sfull[2], pfull[2], odone[2];
+    __shared__ uint64_t qfull, qempty, full[ST], empty[ST], sfull[2], pfull[2][2], odone[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
@@ -461,7 +468,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 128);
+            mbar_init(&pfull[i][0], 128);
+            mbar_init(&pfull[i][1], 128);
             mbar_init(&odone[i], 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
     };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 0) {
             // ------------------------------ TMA producer ------------------------------
             int tile = 0, nq = 0;  // tiles of the ring, and queries, so far
@@ -602,14 +610,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     const bool more = i + 1 < u.nblk;
                     for (int h = 0; h < tiles && ok; ++h) {
                         if (h == 0) ok = mbar_wait(&full[sv], vph, status, abort_flag);
-                        ok = ok && mbar_wait(&pfull[h], blk[h] & 1, status, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
                         const uint32_t v0 = smem_u32(sRing + sv * TB);
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            ok = mbar_wait(&pfull[h][half], blk[h] & 1, status, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of each atom of V
-                            mma_ts(tmem + 256 + h * D, tmem + h * 128 + kk * 8, desc_mn(v0 + kk * 2048, AB), idesc_o,
-                                   i > 0 || kk > 0);
+                            for (int k4 = 0; k4 < 4; ++k4) {  // 16 keys: 8 columns of P, 2 KB of each atom of V
+                                const int kk = half * 4 + k4;
+                                mma_ts(tmem + 256 + h * D, tmem + h * 128 + kk * 8, desc_mn(v0 + kk * 2048, AB), idesc_o,
+                                       i > 0 || kk > 0);
+                            }
+                        }
+                        if (!ok) break;
                         umma_commit(&odone[h]);
                         ++blk[h];
                         if (more) {
@@ -634,7 +647,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
         __syncwarp();
     } else {
         // ------------------------------ softmax and output ----------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int h = (warp - 4) >> 2;  // this warpgroup's tile
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -679,14 +692,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     break;
                 }
                 tc_fence_after();
-                uint32_t sr[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, sr[c]);
-                tmem_ld_wait();
                 float low = -FLT_MAX;  // a row that has seen a key has a finite maximum
                 const bool whole = !bad && key0 + kKeys - 1 <= pmin &&
                                    (a.window <= 0 || key0 > pmax - a.window || key0 + kKeys <= a.sinks);
                 if (!whole) {
+                    // V: zero the rows that no query of the unit sees; look for
+                    // NaN and infinities in the others
+                    const int vt = vtile + 2 * i + 1, s = vt % ST;
+                    ok = mbar_wait(&full[s], (vt / ST) & 1, status, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll 2
+                    for (int e = row; e < kKeys * (D / 8); e += 128) {
+                        const int key = key0 + ((e >> 3) & (kKeys - 1));
+                        uint4* v = reinterpret_cast<uint4*>(sRing + s * TB) + e;
+                        const bool used = key <= span.pmax && (a.window <= 0 || key > span.pmin - a.window || key < a.sinks);
+                        if (!used)
+                            *v = make_uint4(0, 0, 0, 0);
+                        else
+                            poison |= nonfinite8<T>(*v);
+                    }
+                    fence_async_smem();
+                    // S: -inf where the row does not see the key, 32 columns at a
+                    // time and back to tensor memory, so that the registers hold
+                    // the 128 scores only once (a spill goes to L2: shared memory
+                    // leaves no L1)
                     uint32_t pages = 0xff;  // bit per box: has a page
                     if (bad) {
                         pages = 0;
@@ -698,46 +730,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                             }
                         }
                     }
-                    const int last = pos - key0;                                                   // seen: c <= last
-                    const int first = a.window > 0 ? max(pos - a.window, -1) - key0 : -1;          // and c > first
-                    const int sink = a.window > 0 ? max(min(a.sinks - key0, kKeys), 0) : 0;        // or c < sink
+                    const int last = pos - key0;                                             // seen: x <= last
+                    const int first = a.window > 0 ? max(pos - a.window, -1) - key0 : -1;    // and x > first
+                    const int sink = a.window > 0 ? max(min(a.sinks - key0, kKeys), 0) : 0;  // or x < sink
                     const int box_log2 = 31 - __clz(t.box_keys);
                     bool any = false;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tmem_ld_32x32b_x32(tS + c * 32, x);
+                        // the row's seen columns of this chunk as bits
+                        const int lo = c * 32;
+                        const uint32_t below = last - lo >= 31 ? ~0u : last < lo ? 0u : (2u << (last - lo)) - 1;
+                        const uint32_t after = first < lo ? ~0u : first - lo >= 31 ? 0u : ~((2u << (first - lo)) - 1);
+                        const uint32_t sinks = sink <= lo ? 0u : sink - lo >= 32 ? ~0u : (1u << (sink - lo)) - 1;
+                        uint32_t see = below & (after | sinks);
+                        if (bad)
+                            for (int e = 0; e < 32; e += 16)  // pages hold 16 keys or more
+                                if (!((pages >> ((lo + e) >> box_log2)) & 1u)) see &= ~(0xffffu << e);
+                        any |= see != 0;
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int x = c * 32 + e;
-                            const bool see = x <= last && (x > first || x < sink) && ((pages >> (x >> box_log2)) & 1u);
-                            if (!see) sr[c][e] = 0xff800000u;  // -inf
-                            any |= see;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!((see >> e) & 1u)) x[e] = 0xff800000u;  // -inf
+                        tmem_st_32x32b_x32(tS + c * 32, x);
+                    }
+                    tmem_st_wait();
                     if (!any) low = -INFINITY;
-                    // V: zero the rows that no query of the unit sees; look for
-                    // NaN and infinities in the others
-                    const int vt = vtile + 2 * i + 1, s = vt % ST;
-                    ok = mbar_wait(&full[s], (vt / ST) & 1, status, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int e = row; e < kKeys * (D / 8); e += 128) {
-                        const int key = key0 + ((e >> 3) & (kKeys - 1));
-                        uint4* v = reinterpret_cast<uint4*>(sRing + s * TB) + e;
-                        const bool used = key <= span.pmax && (a.window <= 0 || key > span.pmin - a.window || key < a.sinks);
-                        if (!used)
-                            *v = make_uint4(0, 0, 0, 0);
-                        else
-                            poison |= nonfinite8<T>(*v);
-                    }
-                    fence_async_smem();
                 }
+                uint32_t sr[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, sr[c]);
+                tmem_ld_wait();
                 // maximum of the row (the reference moves only if it grew by 2^kLazy)
-                float mx = low;
+                float mc[4];  // four chains, three-input maxima
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    mc[c] = max3(low, __uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(sr[c][e]));
+                    for (int e = 2; e < 32; e += 2) mc[c] = max3(mc[c], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
+                }
+                const float mx = max3(mc[0], mc[1], fmaxf(mc[2], mc[3]));
                 const bool grow = (mx - m) * a.qscale > kLazy;  // from -inf: always
                 float f = 1.0f;
                 if (grow) {
@@ -765,7 +798,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 }
                 const float ms = kOff<T> - (m == -INFINITY ? 0.0f : m) * a.qscale;  // nothing seen yet: all weights 0
                 const uint64_t qs2 = pack_f32x2(a.qscale, a.qscale), ms2 = pack_f32x2(ms, ms);
-                uint64_t l2 = 0;
+                uint64_t l2[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t p[32];
@@ -774,15 +807,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                         const uint32_t* s2 = &sr[2 * c + (e >> 4)][(2 * e) & 31];
                         const uint64_t x = fma_f32x2((static_cast<uint64_t>(s2[1]) << 32) | s2[0], qs2, ms2);
                         const float p0 = ex2(lo_f32(x)), p1 = ex2(hi_f32(x));
-                        l2 = add_f32x2(l2, pack_f32x2(p0, p1));
+                        l2[e & 3] = add_f32x2(l2[e & 3], pack_f32x2(p0, p1));
                         p[e] = pack2<T>(p0, p1);
                     }
                     tmem_st_32x32b_x32(tS + c * 32, p);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&pfull[h][c]);  // 64 keys' weights: their half of the product may start
                 }
-                l += lo_f32(l2) + hi_f32(l2);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&pfull[h]);
+                const uint64_t ls = add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3]));
+                l += lo_f32(ls) + hi_f32(ls);
             }
             vtile += 2 * u.nblk;
             if (u.nblk > 0 && ok) {
