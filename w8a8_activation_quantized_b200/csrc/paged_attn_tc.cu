@@ -57,20 +57,23 @@ namespace {
 constexpr int kKeys = 128;                     // keys per block
 constexpr int kTcThreads = 384;                // warps 0-3: TMA, MMA, two idle; then a softmax warpgroup per tile
 constexpr int kPlanThreads = 1024;
-constexpr int kMaxPieces = 32;
-constexpr int kSlotsPerSm = 2;                 // places for pieces' partial results, per SM
+constexpr int kMaxGrid = 256;                  // CTAs of the tile kernel: one per SM
+constexpr int kMaxCut = 2560;                  // units up to which they may be cut
+constexpr int kMinShare = 2;                   // blocks per CTA where they are cut
 constexpr float kLazy = 8.0f;                  // log2 of the growth of a maximum that is put off
 
 // One unit: tokens [token0, token0 + ntok) of q's rows, the first at position
 // pmin, against blocks [vb0, vb0 + nblk) of its span; slot -1: the whole span.
 struct __align__(16) TcUnit {
-    int b, token0, ntok, pmin, vb0, nblk, slot, pad;
+    int b, token0, ntok, pmin, vb0, nblk, slot, head;  // head: where the list is cut
 };
-struct __align__(16) TcJoin {
-    int token0, ntok, slot, pieces;  // slot of (piece, head) = slot + piece * H_kv + head
+// A unit of several pieces: the first in `slot`, the others in slot 2 c of the
+// CTAs c behind cta.
+struct TcJoin {
+    int token0, ntok, head, slot, cta, pieces;
 };
 struct TcPlan {
-    int units, joins;  // records, each for H_kv heads
+    int units, cut, joins;  // whole: records, each for H_kv heads
 };
 
 struct TcArgs {
@@ -83,8 +86,10 @@ struct TcArgs {
     TcPlan* plan;
     TcUnit* units;
     TcJoin* joins;
+    int2* ranges;         // cut: each CTA's first record and their number
     float* part;          // [slot][256][D], then [slot][256] maximum and sum
     int slots;
+    int64_t l2_keys;      // keys whose K and V (all heads) fill 3/5 of the L2
 };
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, PTX ex2.approx (relative error near 2^-22)
@@ -108,153 +113,170 @@ __device__ __forceinline__ int span_blocks(const PagedAttnArgs& a, int pmin, int
     return s.blocks;
 }
 
+// Two ways to share the units out.  Whole: the list is sorted, longest first,
+// and each CTA takes its units in snake order.  Cut: the units' blocks form one
+// line, in order, of which each CTA takes an equal share; a unit that several
+// share leaves fp32 partial results, at most two per CTA, for the join.  The
+// cheaper one is taken, in blocks: whole, the longest CTA; cut, the share, the
+// start and end of a unit (about two blocks each) once more per CTA, and eight
+// for writing and joining the partial results.  With units for every SM the cut
+// also needs the keys and values to stay in the L2: whole units of the same
+// head walk through its keys together and read them from HBM once, the cut ones
+// start all over the place (four chunks of 500 over 268 MB of keys and values:
+// 278 us whole, 305 us cut; 4096 tokens over 67 MB: 940 us whole, 917 us cut).
 __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
-    extern __shared__ int32_t pre[];  // [B + 1] tiles before each request
+    extern __shared__ int32_t pre[];  // [B + 1] tiles before each request, then [B] of each request's row, tokens and keys
     __shared__ int64_t s_warp[kPlanThreads / 32];
-    __shared__ int s_hist[1024];
-    __shared__ float s_cost[kMaxPieces];
-    __shared__ int s_max, s_chunk, s_slot, s_joins;
-    __shared__ unsigned long long s_work;
+    __shared__ int s_hist[kPlanThreads], s_sorted[kMaxCut];
+    __shared__ int s_first[kMaxGrid], s_last[kMaxGrid];
+    __shared__ int s_max, s_joins;
+    __shared__ unsigned long long s_keys;
     const PagedAttnArgs& a = t.p;
-    const int per_unit = 2 * t.tok;
+    const int per_unit = 2 * t.tok, tid = threadIdx.x, lane = tid & 31;
+    int32_t* start = pre + a.B + 1;
+    int32_t* fresh = start + a.B;
+    int32_t* keys = fresh + a.B;
     pdl_wait();
     pdl_trigger();
-    s_hist[threadIdx.x] = 0;
-    if (threadIdx.x == 0) {
-        s_max = s_slot = s_joins = 0;
-        s_work = 0;
+    s_hist[tid] = 0;
+    if (tid == 0) {
+        s_max = s_joins = 0;
+        s_keys = 0;
+    }
+    if (tid < kMaxGrid) {
+        s_first[tid] = INT_MAX;
+        s_last[tid] = -1;
     }
     const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
-    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int sum = 0;
+    int64_t len = 0;
     bool any_bad = false;
     for (int b = b0; b < b1; ++b) {
         bool bad;
         const PagedRequest r = paged_request(a, b, &bad);
         any_bad |= bad;
+        len += r.n > 0 ? r.L : 0;
         pre[b] = sum;
+        start[b] = r.start;
+        fresh[b] = r.n;
+        keys[b] = r.L;
         sum += (r.n + per_unit - 1) / per_unit;
     }
     if (any_bad) atomicOr(a.status, kStatusIndex);
     int64_t total;
     const int base = static_cast<int>(block_prefix<kPlanThreads>(sum, s_warp, &total));
     for (int b = b0; b < b1; ++b) pre[b] += base;
-    if (threadIdx.x == 0) pre[a.B] = static_cast<int>(total);
+    if (tid == 0) pre[a.B] = static_cast<int>(total);
     __syncthreads();
     const int tiles = static_cast<int>(total);
     auto unit = [&](int i) {
         TcUnit u;
         u.b = find_request(pre, a.B, i);
-        bool bad;
-        const PagedRequest r = paged_request(a, u.b, &bad);
         const int first = (i - pre[u.b]) * per_unit;
-        u.token0 = r.start + first;
-        u.ntok = min(per_unit, r.n - first);
-        u.pmin = r.L - r.n + first;
+        u.token0 = start[u.b] + first;
+        u.ntok = min(per_unit, fresh[u.b] - first);
+        u.pmin = keys[u.b] - fresh[u.b] + first;
         u.vb0 = 0;
         u.nblk = span_blocks(a, u.pmin, u.ntok);
         u.slot = -1;
-        u.pad = 0;
+        u.head = 0;
         return u;
     };
+    // this thread's tiles, in order, and the blocks before them
+    const int each = (tiles + kPlanThreads - 1) / kPlanThreads;
+    const int i0 = min(tiles, tid * each), i1 = min(tiles, i0 + each);
     int mx = 0;
-    unsigned long long work = 0;
-    for (int i = threadIdx.x; i < tiles; i += kPlanThreads) {
+    int64_t blocks = 0;
+    for (int i = i0; i < i1; ++i) {
         const int n = unit(i).nblk;
         mx = max(mx, n);
-        work += n;
+        blocks += n;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        work += __shfl_xor_sync(0xffffffffu, work, o);
-    }
-    if ((threadIdx.x & 31) == 0) {
-        atomicMax(&s_max, mx);
-        atomicAdd(&s_work, work);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (lane == 0) atomicMax(&s_max, mx);
+    if (len) atomicAdd(&s_keys, static_cast<unsigned long long>(len));
+    int64_t work;
+    int64_t before = block_prefix<kPlanThreads>(blocks, s_warp, &work);
+    mx = s_max;
+    // whole: places by counting per class of length
+    const float scale = (kPlanThreads - 1.0f) / max(1, mx);
+    auto bin = [&](int n) { return kPlanThreads - 1 - min(kPlanThreads - 1, static_cast<int>(n * scale)); };
+    for (int i = i0; i < i1; ++i) atomicAdd(&s_hist[bin(unit(i).nblk)], 1);
+    __syncthreads();
+    const int64_t place = block_prefix<kPlanThreads>(s_hist[tid], s_warp, &total);
+    s_hist[tid] = static_cast<int>(place);
+    __syncthreads();
+    const int64_t units = static_cast<int64_t>(tiles) * a.c.H_kv;
+    const bool may_cut = units <= kMaxCut;  // beyond, the rounds are many and even out
+    for (int i = i0; i < i1; ++i) {
+        const TcUnit u = unit(i);
+        const int at = atomicAdd(&s_hist[bin(u.nblk)], 1);
+        t.units[at] = u;
+        if (may_cut) s_sorted[at] = u.nblk;
     }
     __syncthreads();
-    mx = s_max;
-    // How long a piece may be.  Units enough for two rounds of the SMs: whole
-    // spans.  Fewer: warp w tries the longest span cut into w + 1; the cost of a
-    // cut is the longest piece, or the rounds' average, in blocks, plus about
-    // two blocks per unit to start and end it and four for the join.
-    const int64_t whole_units = static_cast<int64_t>(tiles) * a.c.H_kv;
-    if (whole_units < 2 * t.grid && mx > 1) {
-        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        const int chunk = (mx + w) / (w + 1);
-        int pieces = 0;
-        for (int i = lane; i < tiles; i += 32) pieces += max(1, (unit(i).nblk + chunk - 1) / chunk);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
-        if (lane == 0) {
-            const int64_t units = static_cast<int64_t>(pieces) * a.c.H_kv;
-            const int64_t rounds = (units + t.grid - 1) / t.grid;
-            const float avg = static_cast<float>(s_work) * a.c.H_kv / units;
-            float cost = fmaxf(chunk, rounds * avg) + 2.0f * rounds + (w > 0 ? 4.0f : 0.0f);
-            if (w > 0 && units > t.slots) cost = FLT_MAX;  // no place for the partial results
-            s_cost[w] = cost;
+    work *= a.c.H_kv;
+    const int64_t share = max(static_cast<int64_t>(kMinShare), (work + t.grid - 1) / t.grid);
+    bool cut = false;
+    if (may_cut) {
+        int load = 0;
+        if (tid < t.grid)
+            for (int r = 0; r * t.grid < units; ++r) {
+                const int x = r * t.grid + ((r & 1) ? t.grid - 1 - tid : tid);
+                if (x < units) load += s_sorted[x / a.c.H_kv] + 2;
+            }
+        load = __reduce_max_sync(0xffffffffu, load);
+        __syncthreads();
+        if (tid == 0) s_max = 0;
+        __syncthreads();
+        if (lane == 0) atomicMax(&s_max, load);
+        __syncthreads();
+        cut = share + 2 * ((units + t.grid - 1) / t.grid + 1) + 8 < s_max &&
+              (units < t.grid || static_cast<int64_t>(s_keys) <= t.l2_keys);
+    }
+    if (cut) {
+        // Record j + c is unit j's piece in CTA c's share (so a CTA's records are
+        // next to one another); a unit without blocks has one all the same.
+        for (int i = i0; i < i1; ++i) {
+            TcUnit u = unit(i);
+            const int n = u.nblk;
+            for (int head = 0; head < a.c.H_kv; ++head) {
+                const int64_t x0 = before * a.c.H_kv + static_cast<int64_t>(head) * n, x1 = x0 + n;
+                const int j = i * a.c.H_kv + head;
+                const int c0 = static_cast<int>(min(x0 / share, static_cast<int64_t>(t.grid - 1)));
+                const int c1 = n > 0 ? static_cast<int>((x1 - 1) / share) : c0;
+                u.head = head;
+                const int slot0 = 2 * c0 + (x0 == c0 * share ? 0 : 1);
+                for (int c = c0; c <= c1; ++c) {
+                    const int64_t y0 = max(x0, c * share), y1 = min(x1, (c + 1) * share);
+                    u.vb0 = static_cast<int>(y0 - x0);
+                    u.nblk = n > 0 ? static_cast<int>(y1 - y0) : 0;
+                    u.slot = c1 == c0 ? -1 : c == c0 ? slot0 : 2 * c;
+                    t.units[j + c] = u;
+                    atomicMin(&s_first[c], j + c);
+                    atomicMax(&s_last[c], j + c);
+                }
+                if (c1 > c0) t.joins[atomicAdd(&s_joins, 1)] = TcJoin{u.token0, u.ntok, head, slot0, c0, c1 - c0 + 1};
+            }
+            before += n;
         }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            int best = 0;
-            for (int i = 1; i < kMaxPieces; ++i)
-                if (s_cost[i] < s_cost[best]) best = i;
-            s_chunk = (mx + best) / (best + 1);
-        }
-    } else if (threadIdx.x == 0) {
-        s_chunk = max(mx, 1);
+        if (tid < t.grid) t.ranges[tid] = make_int2(s_first[tid], s_last[tid] < 0 ? 0 : s_last[tid] - s_first[tid] + 1);
     }
-    __syncthreads();
-    const int chunk = s_chunk;
-    // longest first: count the pieces per length class, then place them
-    const float scale = 1023.0f / max(1, min(mx, chunk));
-    auto bin = [&](int n) { return 1023 - min(1023, static_cast<int>(n * scale)); };
-    auto piece_len = [&](int n, int k, int q) {  // [q n / k, (q + 1) n / k)
-        return static_cast<int>(static_cast<int64_t>(n) * (q + 1) / k - static_cast<int64_t>(n) * q / k);
-    };
-    for (int i = threadIdx.x; i < tiles; i += kPlanThreads) {
-        const int n = unit(i).nblk, k = max(1, (n + chunk - 1) / chunk);
-        for (int q = 0; q < k; ++q) atomicAdd(&s_hist[bin(piece_len(n, k, q))], 1);
-    }
-    __syncthreads();
-    int64_t all;
-    const int64_t at = block_prefix<kPlanThreads>(s_hist[threadIdx.x], s_warp, &all);
-    s_hist[threadIdx.x] = static_cast<int>(at);
-    __syncthreads();
-    for (int i = threadIdx.x; i < tiles; i += kPlanThreads) {
-        TcUnit u = unit(i);
-        const int n = u.nblk, k = max(1, (n + chunk - 1) / chunk);
-        int slot = -1;
-        if (k > 1) {
-            slot = atomicAdd(&s_slot, k * a.c.H_kv);
-            t.joins[atomicAdd(&s_joins, 1)] = TcJoin{u.token0, u.ntok, slot, k};
-        }
-        for (int q = 0; q < k; ++q) {
-            u.vb0 = static_cast<int>(static_cast<int64_t>(n) * q / k);
-            u.nblk = piece_len(n, k, q);
-            u.slot = k > 1 ? slot + q * a.c.H_kv : -1;
-            t.units[atomicAdd(&s_hist[bin(u.nblk)], 1)] = u;
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) *t.plan = TcPlan{static_cast<int>(all), s_joins};
+    if (tid == 0) *t.plan = TcPlan{tiles, cut ? 1 : 0, s_joins};
 }
 
 // ---- tensor-core pieces ---------------------------------------------------------
 
-// Operand stored with rows of 128 bytes along MN (64 16-bit elements, 128-byte
-// swizzle) and 8-row groups along K 1024 bytes apart; `lbo` bytes between
+// Shared-memory operand descriptors, 128-byte swizzle, as two words: the low
+// one is the start address and the leading byte offset (both >> 4), the high
+// one the stride between 8-row groups (1024 bytes), the version and the layout,
+// which are constants here.  K-major: rows of 64 K elements; the leading offset
+// is not used.  MN-major: rows of 64 MN elements, the leading offset between
 // 64-element atoms along MN.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;  // version
-    d |= static_cast<uint64_t>(2u) << 61;  // SWIZZLE_128B
-    return d;
-}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | (lbo >> 4) << 16; }
 
 // kind::f16 instruction descriptor: D = F32, A = B = fp16 (bf = 0) or bf16 (bf
 // = 1); b_mn: B is MN-major.
@@ -264,22 +286,30 @@ __host__ __device__ constexpr uint32_t idesc_16(int M, int N, int bf, int b_mn) 
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
 }
 // A from tensor memory: row = lane, two 16-bit values of K per column.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x != 0;
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -292,6 +322,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+// Waits for the loads so far; r is given, so that no use of it moves in front.
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -322,9 +358,9 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return d;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {  // NaN if any is
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -461,15 +497,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
     if (threadIdx.x == 0) {
         s_abort = 0;
         mbar_init(&qfull, 1);
-        mbar_init(&qempty, 1);
+        mbar_init(&qempty, 2);
         for (int s = 0; s < ST; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);  // each tile's products
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i][0], 128);
-            mbar_init(&pfull[i][1], 128);
+            mbar_init(&pfull[i][0], 4);  // one arrival per warp
+            mbar_init(&pfull[i][1], 4);
             mbar_init(&odone[i], 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -486,12 +522,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
     pdl_wait();
     pdl_trigger();
     unsigned* status = a.status;
+    const bool cut = t.plan->cut;
     const int nunits = t.plan->units * a.c.H_kv;
-    const int rounds = (nunits + t.grid - 1) / t.grid;
-    // round r of this CTA: snake order over the list, which is sorted
-    auto unit_index = [&](int r) {
+    const int2 range = cut ? t.ranges[blockIdx.x] : make_int2(0, 0);
+    const int rounds = cut ? range.y : (nunits + t.grid - 1) / t.grid;
+    // this CTA's unit of round r, and its head; false: it has none
+    auto fetch = [&](int r, TcUnit& u, int& head) {
+        if (cut) {
+            u = t.units[range.x + r];
+            head = u.head;
+            return true;
+        }
         const int i = static_cast<int>(blockIdx.x);
-        return r * t.grid + ((r & 1) ? t.grid - 1 - i : i);
+        const int x = r * t.grid + ((r & 1) ? t.grid - 1 - i : i);
+        if (x >= nunits) return false;
+        u = t.units[x / a.c.H_kv];
+        head = x % a.c.H_kv;
+        return true;
     };
 
     if (warp < 4) {
@@ -501,11 +548,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             int tile = 0, nq = 0;  // tiles of the ring, and queries, so far
             bool ok = true;
             for (int r = 0; r < rounds && ok; ++r) {
-                const int ui = unit_index(r);
-                if (ui >= nunits) continue;
-                const TcUnit u = t.units[ui / a.c.H_kv];
-                const int head = ui % a.c.H_kv;
-                if (u.nblk == 0) continue;
+                TcUnit u;
+                int head;
+                if (!fetch(r, u, head) || u.nblk == 0) continue;
                 PagedSpan<kKeys> span;
                 span.set(u.pmin, u.pmin + u.ntok - 1, a.window, a.sinks);
                 const int32_t* table = a.table + u.b * a.ld_table;
@@ -572,74 +617,76 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     }
                 }
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // ------------------------------ MMA issuer --------------------------------
+            // The whole warp runs the loop, so that addresses stay in uniform
+            // registers; one lane issues.
             constexpr uint32_t idesc_s = idesc_16(128, kKeys, BF, 0);
             constexpr uint32_t idesc_o = idesc_16(128, D, BF, 1);
+            const uint32_t q_lo = desc_lo(smem_u32(sQ), 0), k_lo = desc_lo(smem_u32(sRing), 0), v_lo = desc_lo(smem_u32(sRing), AB);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const bool leader = elect_one();
             int tile = 0, nq = 0, blk[2] = {0, 0};  // blk: blocks of each tile so far
             bool ok = true;
             for (int r = 0; r < rounds && ok; ++r) {
-                const int ui = unit_index(r);
-                if (ui >= nunits) continue;
-                const TcUnit u = t.units[ui / a.c.H_kv];
-                if (u.nblk == 0) continue;
-                const int tiles = u.ntok > t.tok ? 2 : 1;
+                TcUnit u;
+                int head;
+                if (!fetch(r, u, head)) continue;
+                const int nblk = __shfl_sync(0xffffffffu, u.nblk, 0), tiles = __shfl_sync(0xffffffffu, u.ntok, 0) > t.tok ? 2 : 1;
+                if (nblk == 0) continue;
                 auto scores = [&](int h, int s) {  // S_h = Q_h K^T
-                    const uint32_t a0 = smem_u32(sQ + h * TB), b0 = smem_u32(sRing + s * TB);
+                    if (leader) {
+                        const uint32_t a0 = q_lo + h * (TB >> 4), b0 = k_lo + s * (TB >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * AB + (kk & 3) * 32;
-                        mma_ss(tmem + h * 128, umma_desc_sw128(a0 + off), umma_desc_sw128(b0 + off), idesc_s, kk > 0);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * AB + (kk & 3) * 32) >> 4;
+                            mma_ss(tm + h * 128, a0 + off, b0 + off, idesc_s, kk > 0);
+                        }
+                        umma_commit(&sfull[h]);
                     }
-                    umma_commit(&sfull[h]);
                 };
                 {
                     const int s = tile % ST;
                     ok = mbar_wait(&full[s], (tile / ST) & 1, status, abort_flag) && mbar_wait(&qfull, nq & 1, status, abort_flag);
-                    if (!ok) break;
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
                     for (int h = 0; h < tiles; ++h) scores(h, s);
-                    umma_commit(&empty[s]);
-                    if (u.nblk == 1) umma_commit(&qempty);
                     ++tile;
                 }
                 ++nq;
-                for (int i = 0; i < u.nblk && ok; ++i) {
+                for (int i = 0; i < nblk && ok; ++i) {
                     const int sv = tile % ST, vph = (tile / ST) & 1;
                     const int sk = (tile + 1) % ST, kph = ((tile + 1) / ST) & 1;
-                    const bool more = i + 1 < u.nblk;
-                    for (int h = 0; h < tiles && ok; ++h) {
+                    const bool more = i + 1 < nblk;
+                    for (int h = 0; h < tiles; ++h) {
                         if (h == 0) ok = mbar_wait(&full[sv], vph, status, abort_flag);
-                        const uint32_t v0 = smem_u32(sRing + sv * TB);
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            ok = mbar_wait(&pfull[h][half], blk[h] & 1, status, abort_flag);
-                            if (!ok) break;
-                            tc_fence_after();
+                        const uint32_t v0 = v_lo + sv * (TB >> 4);
 #pragma unroll
-                            for (int k4 = 0; k4 < 4; ++k4) {  // 16 keys: 8 columns of P, 2 KB of each atom of V
-                                const int kk = half * 4 + k4;
-                                mma_ts(tmem + 256 + h * D, tmem + h * 128 + kk * 8, desc_mn(v0 + kk * 2048, AB), idesc_o,
-                                       i > 0 || kk > 0);
+                        for (int half = 0; half < 2; ++half) {
+                            ok = ok && mbar_wait(&pfull[h][half], blk[h] & 1, status, abort_flag);
+                            ok = __all_sync(0xffffffffu, ok);
+                            tc_fence_after();
+                            if (ok && leader) {
+#pragma unroll
+                                for (int k4 = 0; k4 < 4; ++k4) {  // 16 keys: 8 columns of P, 2 KB of each atom of V
+                                    const int kk = half * 4 + k4;
+                                    mma_ts(tm + 256 + h * D, tm + h * 128 + kk * 8, v0 + (kk * 2048 >> 4), idesc_o, i > 0 || kk > 0);
+                                }
                             }
                         }
                         if (!ok) break;
-                        umma_commit(&odone[h]);
+                        if (!more && leader) umma_commit(&odone[h]);
                         ++blk[h];
                         if (more) {
                             if (h == 0) {
                                 ok = mbar_wait(&full[sk], kph, status, abort_flag);
-                                if (!ok) break;
+                                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                                 tc_fence_after();
                             }
                             scores(h, sk);
                         }
                     }
                     if (!ok) break;
-                    umma_commit(&empty[sv]);
-                    if (more) {
-                        umma_commit(&empty[sk]);
-                        if (i + 2 == u.nblk) umma_commit(&qempty);  // the unit's last scores are made
-                    }
                     tile += more ? 2 : 1;
                 }
             }
@@ -652,14 +699,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_addr + h * 128, tO = tmem + lane_addr + 256 + h * D;
-        int nb = 0;    // blocks of this tile so far
+        int nb = 0, nu = 0;  // blocks and units of this tile so far
         int vtile = 0; // the ring's index of the unit's first K tile
         bool ok = true;
         for (int r = 0; r < rounds && ok; ++r) {
-            const int ui = unit_index(r);
-            if (ui >= nunits) continue;
-            const TcUnit u = t.units[ui / a.c.H_kv];
-            const int head = ui % a.c.H_kv;
+            TcUnit u;
+            int head;
+            if (!fetch(r, u, head)) continue;
             const int tok0 = h * t.tok, ntok = min(t.tok, u.ntok - tok0);  // this tile's tokens
             if (ntok <= 0) {
                 vtile += 2 * u.nblk;
@@ -684,6 +730,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             bad = group_or(h, bad);
             float m = -INFINITY, l = 0.0f;
             bool poison = false;
+            // One thread tells the producer what this tile's products are done with
+            // (and for the second tile, where the unit has none).
+            const int frees = row != 0 ? 0 : u.ntok > t.tok ? 1 : 2;
             for (int i = 0; i < u.nblk; ++i, ++nb) {
                 const int key0 = span.block(u.vb0 + i) * kKeys;
                 ok = mbar_wait(&sfull[h], nb & 1, status, abort_flag);
@@ -692,6 +741,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     break;
                 }
                 tc_fence_after();
+                for (int e = 0; e < frees; ++e) {  // QK^T of this block and PV of the last one are done
+                    mbar_arrive(&empty[(vtile + 2 * i) % ST]);
+                    if (i > 0) mbar_arrive(&empty[(vtile + 2 * i - 1) % ST]);
+                    if (i + 1 == u.nblk) mbar_arrive(&qempty);
+                }
                 float low = -FLT_MAX;  // a row that has seen a key has a finite maximum
                 const bool whole = !bad && key0 + kKeys - 1 <= pmin &&
                                    (a.window <= 0 || key0 > pmax - a.window || key0 + kKeys <= a.sinks);
@@ -749,7 +803,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                             for (int e = 0; e < 32; e += 16)  // pages hold 16 keys or more
                                 if (!((pages >> ((lo + e) >> box_log2)) & 1u)) see &= ~(0xffffu << e);
                         any |= see != 0;
-                        tmem_ld_wait();
+                        ld_wait(x);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!((see >> e) & 1u)) x[e] = 0xff800000u;  // -inf
@@ -758,38 +812,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     tmem_st_wait();
                     if (!any) low = -INFINITY;
                 }
-                uint32_t sr[4][32];
+                // Maximum of the row (the reference moves only if it grew by 2^kLazy),
+                // in four chains; the upper 64 columns first, which are read again
+                // for their weights.
+                uint32_t sr[2][32];
+                float mc[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, sr[c]);
-                tmem_ld_wait();
-                // maximum of the row (the reference moves only if it grew by 2^kLazy)
-                float mc[4];  // four chains, three-input maxima
+                for (int half = 1; half >= 0; --half) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mc[c] = max3(low, __uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]));
+                    for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(tS + half * 64 + c * 32, sr[c]);
+                    ld_wait(sr[0]);
+                    ld_wait(sr[1]);
 #pragma unroll
-                    for (int e = 2; e < 32; e += 2) mc[c] = max3(mc[c], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
+                    for (int c = 0; c < 4; ++c) {
+                        if (half) mc[c] = low;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2)
+                            mc[c] = max3_nan(mc[c], __uint_as_float(sr[c >> 1][(c & 1) * 16 + e]), __uint_as_float(sr[c >> 1][(c & 1) * 16 + e + 1]));
+                    }
                 }
-                const float mx = max3(mc[0], mc[1], fmaxf(mc[2], mc[3]));
-                const bool grow = (mx - m) * a.qscale > kLazy;  // from -inf: always
+                const float mx = max3_nan(max3_nan(mc[0], mc[1], mc[2]), mc[3], mc[3]);
+                // From -inf it always moves.  A NaN score makes the row NaN, and so
+                // does +inf (inf - inf), as in the formula.
+                const bool grow = m != mx && !((mx - m) * a.qscale <= kLazy);
                 float f = 1.0f;
                 if (grow) {
                     f = ex2((m - mx) * a.qscale);
-                    m = mx;
+                    m = mx == INFINITY ? NAN : mx;
                     l *= f;
                 }
-                if (i > 0 && __any_sync(0xffffffffu, grow)) {
-                    ok = mbar_wait(&odone[h], (nb - 1) & 1, status, abort_flag);  // O is complete up to the last block
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                if (i > 0 && __any_sync(0xffffffffu, grow)) {  // O is complete up to the last block
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(tO + c * 32, o);
-                        tmem_ld_wait();
+                        ld_wait(o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                         tmem_st_32x32b_x32(tO + c * 32, o);
@@ -802,32 +859,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t p[32];
+                    if (c == 1) {
+                        ld_wait(sr[0]);
+                        ld_wait(sr[1]);
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const uint32_t* s2 = &sr[2 * c + (e >> 4)][(2 * e) & 31];
+                        const uint32_t* s2 = &sr[e >> 4][(2 * e) & 31];
                         const uint64_t x = fma_f32x2((static_cast<uint64_t>(s2[1]) << 32) | s2[0], qs2, ms2);
-                        const float p0 = ex2(lo_f32(x)), p1 = ex2(hi_f32(x));
-                        l2[e & 3] = add_f32x2(l2[e & 3], pack_f32x2(p0, p1));
-                        p[e] = pack2<T>(p0, p1);
+                        const uint64_t w = pack_f32x2(ex2(lo_f32(x)), ex2(hi_f32(x)));
+                        l2[e & 3] = add_f32x2(l2[e & 3], w);
+                        p[e] = pack2<T>(lo_f32(w), hi_f32(w));
                     }
                     tmem_st_32x32b_x32(tS + c * 32, p);
+                    if (c == 0) {
+                        tmem_ld_32x32b_x32(tS + 64, sr[0]);
+                        tmem_ld_32x32b_x32(tS + 96, sr[1]);
+                    }
                     tmem_st_wait();
                     tc_fence_before();
-                    mbar_arrive(&pfull[h][c]);  // 64 keys' weights: their half of the product may start
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[h][c]);  // 64 keys' weights: their half of the product may start
                 }
                 const uint64_t ls = add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3]));
                 l += lo_f32(ls) + hi_f32(ls);
             }
             vtile += 2 * u.nblk;
             if (u.nblk > 0 && ok) {
-                ok = mbar_wait(&odone[h], (nb - 1) & 1, status, abort_flag);
+                ok = mbar_wait(&odone[h], nu & 1, status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
+                for (int e = 0; e < frees; ++e) mbar_arrive(&empty[(vtile - 1) % ST]);
+                ++nu;
             }
             poison = group_or(h, poison);
             ok = !group_or(h, !ok);  // the group's warps go on, or end, together
             if (!ok) break;
-            const int slot = u.slot < 0 ? -1 : u.slot + head;
+            const int slot = u.slot;
             const int64_t q_row = u.token0 + tok0 + tok;
             const int64_t q_col = static_cast<int64_t>(head * a.G + (row - tok * a.G)) * D;
             T* out = static_cast<T*>(a.out) + q_row * a.ld_out + q_col;
@@ -845,7 +913,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 uint32_t o[32];
                 if (u.nblk > 0) {
                     tmem_ld_32x32b_x32(tO + c * 32, o);
-                    tmem_ld_wait();
+                    ld_wait(o);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0;
@@ -883,55 +951,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
     }
 }
 
-// Joins the pieces of the tiles that were cut, a warp per row:
+// Joins the pieces of the units that were cut, a warp per row:
 // out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_paged_tc_join(const TcArgs t) {
+    constexpr int E = D / 32;  // dims per lane
     pdl_wait();
     pdl_trigger();
     const PagedAttnArgs& a = t.p;
     const int lane = threadIdx.x & 31;
-    const int64_t rows = static_cast<int64_t>(t.plan->joins) * a.c.H_kv * 256;
-    for (int64_t x = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; x < rows; x += gridDim.x * 8) {
-        const int row = static_cast<int>(x & 255);
-        const int64_t y = x >> 8;
-        const int head = static_cast<int>(y % a.c.H_kv);
-        const TcJoin j = t.joins[y / a.c.H_kv];
+    const int rows = t.plan->joins * 256;  // at most 256 per CTA of the tile kernel
+    for (int x = static_cast<int>(blockIdx.x * 256 + threadIdx.x) >> 5; x < rows; x += gridDim.x * 8) {
+        const int row = x & 255;
+        const TcJoin j = t.joins[x >> 8];
         const int tok = (row >> 7) * t.tok + (row & 127) / a.G;
         if ((row & 127) >= t.tok * a.G || tok >= j.ntok) continue;
-        float2 ml = make_float2(-INFINITY, 0.0f);
-        if (lane < j.pieces) ml = *part_ml<D>(t, j.slot + lane * a.c.H_kv + head, row);
-        float mx = ml.x;
+        float mx = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float f = ml.x == mx ? 1.0f : ex2((ml.x - mx) * a.qscale);
-        float l = ml.y * f;
+        for (int e = 0; e < E; ++e) o[e] = 0.0f;
+        for (int c0 = 0; c0 < j.pieces; c0 += 4) {  // four pieces' loads at a time
+            float2 ml[4];
+            float v[4][E];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float o[D / 32];
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i, slot = c == 0 ? j.slot : 2 * (j.cta + c);
+                ml[i] = make_float2(-INFINITY, 0.0f);
+                if (c < j.pieces) {
+                    ml[i] = *part_ml<D>(t, slot, row);
+                    const float* p = part_row<D>(t, slot, row) + lane * E;
+                    if constexpr (D == 128)
+                        *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(p);
+                    else
+                        *reinterpret_cast<float2*>(v[i]) = *reinterpret_cast<const float2*>(p);
+                }
+            }
+            float mn = mx;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
-#pragma unroll 4
-        for (int c = 0; c < j.pieces; ++c) {
-            const float w = __shfl_sync(0xffffffffu, f, c);
-            const float* p = part_row<D>(t, j.slot + c * a.c.H_kv + head, row) + lane * (D / 32);
-            if constexpr (D == 128) {
-                const float4 v = *reinterpret_cast<const float4*>(p);
-                o[0] = fmaf(v.x, w, o[0]);
-                o[1] = fmaf(v.y, w, o[1]);
-                o[2] = fmaf(v.z, w, o[2]);
-                o[3] = fmaf(v.w, w, o[3]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(p);
-                o[0] = fmaf(v.x, w, o[0]);
-                o[1] = fmaf(v.y, w, o[1]);
+            for (int i = 0; i < 4; ++i) mn = fmaxf(mn, ml[i].x);
+            const float f = mn == mx ? 1.0f : ex2((mx - mn) * a.qscale);
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= f;
+            mx = mn;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (c0 + i >= j.pieces) break;
+                const float w = ml[i].x == mx ? 1.0f : ex2((ml[i].x - mx) * a.qscale);
+                l = fmaf(ml[i].y, w, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(v[i][e], w, o[e]);
             }
         }
         const float inv = mx == -INFINITY ? 0.0f : 1.0f / l;
         T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(j.token0) + tok) * a.ld_out +
-                 static_cast<int64_t>(head * a.G + (row & 127) % a.G) * D + lane * (D / 32);
+                 static_cast<int64_t>(j.head * a.G + (row & 127) % a.G) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack2<T>(o[e] * inv, o[e + 1] * inv);
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack2<T>(o[e] * inv, o[e + 1] * inv);
     }
 }
 
@@ -941,15 +1016,17 @@ int64_t max_tiles(int64_t T, int64_t B, int tok) { return T / (2 * tok) + B; }
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct TcLayout {
-    size_t units, joins, part, total;
+    size_t ranges, units, joins, part, total;
 };
 TcLayout tc_layout(int64_t T, int64_t B, int G, int D, int num_sms) {
     const int tok = 128 / G;
-    const int64_t slots = static_cast<int64_t>(kSlotsPerSm) * num_sms;
+    const int grid = std::min(num_sms, kMaxGrid);
+    const int64_t slots = 2 * grid;
     TcLayout l;
-    l.units = 256;
-    l.joins = l.units + align256((max_tiles(T, B, tok) + slots) * sizeof(TcUnit));
-    l.part = l.joins + align256(slots * sizeof(TcJoin));
+    l.ranges = 256;
+    l.units = l.ranges + align256(grid * sizeof(int2));
+    l.joins = l.units + align256((std::max<int64_t>(max_tiles(T, B, tok), kMaxCut) + grid) * sizeof(TcUnit));
+    l.part = l.joins + align256(grid * sizeof(TcJoin));  // a cut unit ends at some CTA's share
     l.total = l.part + slots * 256 * (D + 2) * sizeof(float);
     return l;
 }
@@ -961,13 +1038,18 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
     t.tok = 128 / p.G;
     t.box_keys = std::min(p.c.page_size, kKeys);
     t.boxes = kKeys / t.box_keys;
-    t.grid = num_sms;
-    t.slots = kSlotsPerSm * num_sms;
+    t.grid = std::min(num_sms, kMaxGrid);
+    t.slots = 2 * t.grid;
+    int dev = 0, l2 = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (e = cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev)) != cudaSuccess) return e;
+    t.l2_keys = static_cast<int64_t>(l2) * 3 / 5 / (int64_t(4) * D * p.c.H_kv);
     const TcLayout l = tc_layout(p.T, p.B, p.G, D, num_sms);
     char* ws = reinterpret_cast<char*>(p.part);
     t.plan = reinterpret_cast<TcPlan*>(ws);
     t.units = reinterpret_cast<TcUnit*>(ws + l.units);
     t.joins = reinterpret_cast<TcJoin*>(ws + l.joins);
+    t.ranges = reinterpret_cast<int2*>(ws + l.ranges);
     t.part = reinterpret_cast<float*>(ws + l.part);
 
     // Cache maps: dims {D, then token, head and page by ascending stride}.
@@ -1000,11 +1082,13 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
 
     const int smem = 1024 + (2 + kStages<D>) * kTileBytes<D>;
     auto kern = k_paged_tc<T, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if ((e = launch_pdl(k_paged_plan, dim3(1), dim3(kPlanThreads), (p.B + 1) * 4, st, t)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    const int plan_smem = (4 * p.B + 1) * 4;
+    if ((e = cudaFuncSetAttribute(k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_smem)) != cudaSuccess) return e;
+    if ((e = launch_pdl(k_paged_plan, dim3(1), dim3(kPlanThreads), plan_smem, st, t)) != cudaSuccess) return e;
     if ((e = launch_pdl(kern, dim3(num_sms), dim3(kTcThreads), smem, st, tmQ, tmK, tmV, t)) != cudaSuccess) return e;
-    return launch_pdl(k_paged_tc_join<T, D>, dim3(2 * num_sms), dim3(256), 0, st, t);
+    // as many CTAs as are resident: a row is a few dependent loads
+    return launch_pdl(k_paged_tc_join<T, D>, dim3(6 * num_sms), dim3(256), 0, st, t);
 }
 
 }  // namespace
