@@ -26,7 +26,7 @@ def _cache(**kw):
     a = dict(k=64 * MB, v=128 * MB, dt=0, num_pages=64, page_size=16, H_kv=8, D=128, stride_page=16384, stride_head=2048,
              stride_token=128)
     a.update(kw)
-    return cider._PagedCache(*(a[n] for n, _ in cider._PagedCache._fields_))
+    return cider._CACHE.pack(*a.values())
 
 
 def _attend(lib, cache=None, **kw):
@@ -34,7 +34,7 @@ def _attend(lib, cache=None, **kw):
              window=0, sinks=0, scale=0.1, out=5 * MB, ld_out=4096, ws=256 * MB, wsb=64 * MB)
     a.update(kw)
     c = _cache() if cache is None else cache
-    return lib.cider_paged_attention(ctypes.addressof(c), _p(a["q"]), a["ld_q"], a["T"], a["H_q"], _p(a["cu"]), _p(a["kv"]),
+    return lib.cider_paged_attention(c, _p(a["q"]), a["ld_q"], a["T"], a["H_q"], _p(a["cu"]), _p(a["kv"]),
                                      a["B"], _p(a["table"]), a["ld_table"], a["width"], a["max_fresh"], a["window"],
                                      a["sinks"], a["scale"], _p(a["out"]), a["ld_out"], _p(a["ws"]), a["wsb"], None)
 
@@ -50,7 +50,7 @@ def test_bad_caches_are_refused(lib, kw):
     assert _attend(lib, _cache(**kw)) == 1
     assert lib.cider_last_error()
     c = _cache(**kw)
-    assert lib.cider_paged_append(ctypes.addressof(c), _p(MB), 1024, _p(2 * MB), 1024, _p(3 * MB), 4, None) == 1
+    assert lib.cider_paged_append(c, _p(MB), 1024, _p(2 * MB), 1024, _p(3 * MB), 4, None) == 1
 
 
 @pytest.mark.parametrize("kw", [
@@ -80,16 +80,16 @@ def test_bad_append_arguments_are_refused(lib, kw):
     a = dict(k=MB, ld_k=1024, v=2 * MB, ld_v=1024, slots=3 * MB, T=4)
     a.update(kw)
     c = _cache()
-    assert lib.cider_paged_append(ctypes.addressof(c), _p(a["k"]), a["ld_k"], _p(a["v"]), a["ld_v"], _p(a["slots"]), a["T"],
+    assert lib.cider_paged_append(c, _p(a["k"]), a["ld_k"], _p(a["v"]), a["ld_v"], _p(a["slots"]), a["T"],
                                   None) == 1
     assert lib.cider_last_error()
 
 
 def test_append_refuses_one_buffer_for_k_and_v_and_takes_no_rows(lib):
     c = _cache(v=64 * MB)
-    assert lib.cider_paged_append(ctypes.addressof(c), _p(MB), 1024, _p(2 * MB), 1024, _p(3 * MB), 4, None) == 1
+    assert lib.cider_paged_append(c, _p(MB), 1024, _p(2 * MB), 1024, _p(3 * MB), 4, None) == 1
     c = _cache()
-    assert lib.cider_paged_append(ctypes.addressof(c), None, 0, None, 0, None, 0, None) == 0
+    assert lib.cider_paged_append(c, None, 0, None, 0, None, 0, None) == 0
     assert _attend(lib, T=0, q=None, out=None) == 0
 
 

@@ -11,6 +11,7 @@ caller does not pass are allocated with ``torch.empty`` on the input's device.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -448,28 +449,43 @@ def cider_test_set_gemm_variant(variant: int):
 
 
 # ---- paged key/value cache -------------------------------------------------
+# A decode step's kernels take a few microseconds, so these wrappers spend as
+# few as they can: checks that cost no call into torch, one allocation, one
+# look at the current device and stream.
 
-class _PagedCache(ctypes.Structure):  # cider_paged_cache_t
-    _fields_ = [("k", _P), ("v", _P), ("dt", _INT), ("num_pages", _I64), ("page_size", _I64), ("H_kv", _I64),
-                ("D", _I64), ("stride_page", _I64), ("stride_head", _I64), ("stride_token", _I64)]
+_CACHE = struct.Struct("PPi4xqqqqqqq")  # cider_paged_cache_t
 
 
 def _paged_cache(k_cache, v_cache):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or \
-            k_cache.dtype != v_cache.dtype or k_cache.stride(3) != 1:
+    """cider_paged_cache_t as bytes, and H_kv, D."""
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides or v_cache.dtype != k_cache.dtype or \
+            strides[3] != 1:
         raise ValueError("k_cache and v_cache are [num_pages, H_kv, page_size, D] of one dtype, with the same strides "
                          "and unit stride along D")
-    P, H, S, D = k_cache.shape
-    sp, sh, st, _ = k_cache.stride()
-    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _DT[k_cache.dtype], P, S, H, D, sp, sh, st)
+    P, H, S, D = shape
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), _DT[k_cache.dtype], P, S, H, D, *strides[:3]), H, D
 
 
-def _paged_stream(device, stream, tensors):
-    """Checks that every tensor is on `device` and returns the stream's handle."""
+def _on_one_device(index, tensors):
+    if index < 0:
+        raise ValueError("CUDA tensors are needed")
     for t in tensors:
-        if t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}: one device is needed")
-    return _stream(stream, device)
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on one device")
+
+
+def _paged_call(name, index, stream, *args):
+    """Calls `name` with its arguments and the stream (None: the current one) on
+    device `index`."""
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = getattr(lib(), name)(*args, st)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib(), name)(*args, st)
+    if status != 0:
+        _check(name, status)
 
 
 def _empty(shape, dtype, device, stream):
@@ -481,17 +497,26 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _i32(t, name):
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name} must be int32")
-    return _contig(t, name)
+def _int32(tensors, what):
+    for t in tensors:
+        if t.dtype is not torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous int32 tensors")
 
 
 def _packed(t, name, heads, D):
     """[T, heads, D] with dense rows -> its row stride."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D or strides[2] != 1 or (heads > 1 and strides[1] != D):
         raise ValueError(f"{name} is [T, {heads}, {D}] with dense rows (any row stride)")
-    return t.stride(0)
+    return strides[0]
+
+
+def _table(block_table, B):
+    """int32 [B, width] with dense rows -> its row stride and width."""
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1 or \
+            block_table.dtype is not torch.int32:
+        raise ValueError("block_table is int32 [B, width] with dense rows")
+    return block_table.stride(0), block_table.shape[1]
 
 
 def cider_paged_tables(cached, fresh, free_pages, block_table, page_size, num_pages, rows, cu_fresh=None, kv_len=None,
@@ -500,31 +525,28 @@ def cider_paged_tables(cached, fresh, free_pages, block_table, page_size, num_pa
     each request has in the cache and brings; free_pages: int32 pages, taken in
     order; block_table: int32 [B, width], filled behind the pages that each
     request has; rows: rows of the packed batch.
-    -> (cu_fresh [B + 1], kv_len [B], slots [rows], taken [1]), all int32."""
-    dev = block_table.device
-    B = cached.shape[0]
-    if fresh.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1 or \
-            block_table.dtype != torch.int32:
-        raise ValueError("cached and fresh are [B], block_table is int32 [B, width] with dense rows")
-    if cu_fresh is None:
-        cu_fresh = _empty((B + 1,), torch.int32, dev, stream)
-    if kv_len is None:
-        kv_len = _empty((B,), torch.int32, dev, stream)
-    if slots is None:
-        slots = _empty((rows,), torch.int32, dev, stream)
-    if taken is None:
-        taken = _empty((1,), torch.int32, dev, stream)
+    -> (cu_fresh [B + 1], kv_len [B], slots [rows], taken [1]), all int32; the
+    ones that are not given share one allocation."""
+    B = cached.numel()
+    ld, width = _table(block_table, B)
+    if fresh.numel() != B:
+        raise ValueError("cached and fresh are [B]")
+    sizes = (B + 1, B, rows, 1)
+    out = [cu_fresh, kv_len, slots, taken]
+    if any(t is None for t in out):
+        need = [n for n, t in zip(sizes, out) if t is None]
+        parts = iter(_empty(sum(need), torch.int32, block_table.device, stream).split_with_sizes(need))
+        out = [next(parts) if t is None else t for t in out]
+    cu_fresh, kv_len, slots, taken = out
     if cu_fresh.numel() != B + 1 or kv_len.numel() != B or slots.numel() != rows or taken.numel() != 1:
         raise ValueError("cu_fresh is [B + 1], kv_len [B], slots [rows] and taken [1]")
-    for t, name in ((cached, "cached"), (fresh, "fresh"), (free_pages, "free_pages"), (cu_fresh, "cu_fresh"),
-                    (kv_len, "kv_len"), (slots, "slots"), (taken, "taken")):
-        _i32(t, name)
-    st = _paged_stream(dev, stream, (cached, fresh, free_pages, cu_fresh, kv_len, slots, taken))
-    with torch.cuda.device(dev):
-        _check("cider_paged_tables", lib().cider_paged_tables(
-            cached.data_ptr(), fresh.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(), num_pages, page_size,
-            block_table.data_ptr(), block_table.stride(0), block_table.shape[1], cu_fresh.data_ptr(), kv_len.data_ptr(),
-            slots.data_ptr(), rows, taken.data_ptr(), st))
+    given = (cached, fresh, free_pages, cu_fresh, kv_len, slots, taken)
+    _int32(given, "cached, fresh, free_pages, cu_fresh, kv_len, slots and taken")
+    index = block_table.get_device()
+    _on_one_device(index, given)
+    _paged_call("cider_paged_tables", index, stream, cached.data_ptr(), fresh.data_ptr(), B, free_pages.data_ptr(),
+                free_pages.numel(), num_pages, page_size, block_table.data_ptr(), ld, width, cu_fresh.data_ptr(),
+                kv_len.data_ptr(), slots.data_ptr(), rows, taken.data_ptr())
     return cu_fresh, kv_len, slots, taken
 
 
@@ -532,17 +554,18 @@ def cider_paged_append(k_new, v_new, k_cache, v_cache, slots, stream=None):
     """Writes new keys and values ([T, H_kv, D], any row stride) into the cache
     ([num_pages, H_kv, page_size, D], any strides) at slots (int32 [T]; -1
     skips)."""
-    cache = _paged_cache(k_cache, v_cache)
+    cache, H, D = _paged_cache(k_cache, v_cache)
     if k_new.dtype != k_cache.dtype or v_new.dtype != k_cache.dtype:
         raise ValueError("k_new, v_new and the cache must have one dtype")
-    ld_k, ld_v = (_packed(t, n, cache.H_kv, cache.D) for t, n in ((k_new, "k_new"), (v_new, "v_new")))
+    ld_k, ld_v = _packed(k_new, "k_new", H, D), _packed(v_new, "v_new", H, D)
     T = k_new.shape[0]
-    if v_new.shape[0] != T or slots.shape != (T,):
+    if v_new.shape[0] != T or slots.numel() != T:
         raise ValueError("k_new, v_new and slots must have the same number of rows")
-    st = _paged_stream(k_cache.device, stream, (v_cache, k_new, v_new, _i32(slots, "slots")))
-    with torch.cuda.device(k_cache.device):
-        _check("cider_paged_append", lib().cider_paged_append(
-            ctypes.addressof(cache), k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v, slots.data_ptr(), T, st))
+    _int32((slots,), "slots")
+    index = k_cache.get_device()
+    _on_one_device(index, (v_cache, k_new, v_new, slots))
+    _paged_call("cider_paged_append", index, stream, cache, k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v,
+                slots.data_ptr(), T)
 
 
 def cider_paged_attention_workspace_bytes(T, B, H_q, H_kv, D, max_fresh) -> int:
@@ -558,34 +581,39 @@ def cider_paged_attention(q, k_cache, v_cache, block_table, cu_fresh, kv_len, ma
     tokens of any one request (default: T).  window > 0: a query sees the last
     `window` keys up to its own, and the first `sinks`.  scale: default
     1 / sqrt(D).  -> out [T, H_q, D]; rows behind the last request are left as
-    they are."""
-    cache = _paged_cache(k_cache, v_cache)
-    T, H_q, D = q.shape
-    ld_q = _packed(q, "q", H_q, cache.D)
+    they are.  Calls that may run at the same time need a workspace each."""
+    cache, H, D = _paged_cache(k_cache, v_cache)
+    if q.dim() != 3:
+        raise ValueError("q is [T, H_q, D]")
+    T, H_q = q.shape[0], q.shape[1]
+    ld_q = _packed(q, "q", H_q, D)
+    index = q.get_device()
+    B = kv_len.numel()
+    ld, width = _table(block_table, B)
+    if cu_fresh.numel() != B + 1:
+        raise ValueError("cu_fresh is [B + 1] and kv_len [B]")
+    _int32((cu_fresh, kv_len), "cu_fresh and kv_len")
     if out is None:
         out = _empty((T, H_q, D), q.dtype, q.device, stream)
-    ld_out = _packed(out, "out", H_q, cache.D)
-    if out.shape != q.shape or q.dtype != k_cache.dtype or out.dtype != q.dtype:
-        raise ValueError("q, out and the cache must have one dtype, and out q's shape")
-    B = kv_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1 or \
-            block_table.dtype != torch.int32 or cu_fresh.numel() != B + 1:
-        raise ValueError("block_table is int32 [B, width] with dense rows, cu_fresh [B + 1], kv_len [B]")
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ld_out = _packed(out, "out", H_q, D)
+    if q.dtype != k_cache.dtype or out.dtype != q.dtype:
+        raise ValueError("q, out and the cache must have one dtype")
+    _on_one_device(index, (k_cache, v_cache, block_table, cu_fresh, kv_len, out))
     if max_fresh is None:
         max_fresh = T
-    dev = q.device
-    st = _paged_stream(dev, stream, (k_cache, v_cache, block_table, _i32(cu_fresh, "cu_fresh"), _i32(kv_len, "kv_len"), out))
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = cider_paged_attention_workspace_bytes(T, B, H_q, cache.H_kv, D, max_fresh)
-            workspace = _empty((max(need, 16),), torch.uint8, dev, stream)
-        elif workspace.device != dev:
-            raise ValueError(f"tensors on {dev} and {workspace.device}: one device is needed")
-        _check("cider_paged_attention", lib().cider_paged_attention(
-            ctypes.addressof(cache), q.data_ptr(), ld_q, T, H_q, cu_fresh.data_ptr(), kv_len.data_ptr(), B,
-            block_table.data_ptr(), block_table.stride(0), block_table.shape[1], max_fresh, window, sinks,
-            D ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), st))
+    if workspace is None:
+        with torch.cuda.device(index):
+            need = cider_paged_attention_workspace_bytes(T, B, H_q, H, D, max_fresh)
+        workspace = _empty((max(need, 16),), torch.uint8, q.device, stream)
+    elif workspace.get_device() != index:
+        raise ValueError("all tensors must be on one device")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _paged_call("cider_paged_attention", index, stream, cache, q.data_ptr(), ld_q, T, H_q, cu_fresh.data_ptr(),
+                kv_len.data_ptr(), B, block_table.data_ptr(), ld, width, max_fresh, window, sinks,
+                D ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, workspace.data_ptr(), workspace.nbytes)
     return out
 
 

@@ -55,6 +55,7 @@ struct PagedAttnArgs {
     float* part;  // workspace
     unsigned* status;
     int grid;  // CTAs of the split kernel, which is also how the merge finds its work
+    int d_tok, d_head;  // which dimension of the cache's tensor maps (1 .. 3) is the token, the head; the page is the third
 };
 
 cudaError_t launch_paged_tables(const PagedTablesArgs& a, int num_sms, cudaStream_t st);

@@ -14,12 +14,15 @@
 // tensor pipe far from its rate: HBM is the bound, and the 128-row tiles of
 // tcgen05 would only add latency.
 //
-// Loads: each warp has its own ring of kStages steps (16 keys of K and of V)
-// in shared memory, filled by 16-byte cp.async, so warps never wait for one
-// another within a tile; two CTAs of four warps per SM keep up to 2 x 4 x 3 x
-// 8 KB = 192 KB in flight.  A key that no query of the tile sees is not read:
-// its piece of the ring is zero-filled, which also keeps what the cache's
-// unwritten slots hold (NaN, infinities) away from the products.
+// Loads: each warp has its own ring of kStages steps (16 keys of K and of V) in
+// shared memory, filled by TMA in boxes of 16 keys x 64 dims (128-byte swizzle,
+// one mbarrier per stage), so warps never wait for one another within a tile;
+// two CTAs of four warps per SM keep up to 2 x 4 x 3 x 8 KB = 192 KB in flight.
+// (With 16-byte cp.async in their place the loads took half of the kernel's
+// instructions: four requests of up to 32K keys 38.7 us, with TMA see below.)
+// Pages that no query of the tile sees are not read.  Where only some keys of a
+// step are seen by any query, the other rows of V are zeroed in shared memory:
+// what the cache's unwritten slots hold may be NaN, and 0 x NaN is not 0.
 //
 // Split: the work of the whole batch is one line of blocks of 64 keys -- per
 // request, per 16-row tile, per KV head, its blocks -- cut into equal pieces,
@@ -59,16 +62,6 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, PTX ex2.approx (relativ
     return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-    const int n = valid ? 16 : 0;  // 0: the 16 bytes of shared memory become zeros, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -81,6 +74,8 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -179,14 +174,21 @@ __device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, const int64_t*
     return t;
 }
 
-// Element offset of row `row` of tile t in q (at ld) or out.
-__device__ __forceinline__ int64_t row_offset(const PagedAttnArgs& a, const Tile& t, int row, int64_t ld) {
-    const int f = t.row0 + row;
+// Element offset of a request's (token, head) row f in q (at ld) or out.
+__device__ __forceinline__ int64_t row_offset(const PagedAttnArgs& a, int start, int head, int f, int64_t ld) {
     const int i = f / a.G;
-    return (t.r.start + i) * ld + static_cast<int64_t>(t.head * a.G + (f - i * a.G)) * a.c.D;
+    return (start + i) * ld + static_cast<int64_t>(head * a.G + (f - i * a.G)) * a.c.D;
 }
 
-// Place of a CTA's partial result: slot 0 or 1 of CTA c.
+// A tile in several pieces, in the record of the CTA that has the first: their
+// number, the first one's slot (the others are in slot 0 of the CTAs behind),
+// and the tile's place in out.  0 pieces: none.
+struct Join {
+    int pieces, slot, start, head, row0, rows;
+};
+
+// Workspace: two places per CTA for partial results (slot 0: the first piece of
+// its share, 1: the last one), their maxima and sums, and a record per CTA.
 template <int D>
 __device__ __forceinline__ float* part_o(const PagedAttnArgs& a, int64_t c, int slot) {
     return a.part + (c * 2 + slot) * (kRows * D);
@@ -196,28 +198,54 @@ __device__ __forceinline__ float2* part_ml(const PagedAttnArgs& a, int64_t c, in
     return reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.grid) * 2 * kRows * D) + (c * 2 + slot) * kRows;
 }
 
+template <int D>
+__device__ __forceinline__ Join* part_join(const PagedAttnArgs& a) {
+    return reinterpret_cast<Join*>(a.part + static_cast<int64_t>(a.grid) * 2 * kRows * (D + 2));
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnArgs a) {
-    constexpr int kChunks = D / 8;                       // 16-byte pieces per key
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __grid_constant__ CUtensorMap tmK,
+                                                                     const __grid_constant__ CUtensorMap tmV,
+                                                                     const __grid_constant__ PagedAttnArgs a) {
     constexpr int kHalf = kStep * D * 2;                 // bytes of K (or V) of one step
-    constexpr int kLoads = kStep * kChunks / 32;         // pieces of K per lane and step
+    constexpr int kAtom = kStep * 128;                   // bytes of 64 dims of it
+    constexpr int kPieces = kStep * (D / 8) / 32;        // 16-byte pieces of V per lane and step
     constexpr int kNd = D / 16;                          // d-steps of 16
     extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t s_full[kWarps][kStages];
+    __shared__ int s_abort;
     __shared__ int64_t s_warp[kWarps];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-    uint8_t* ring = smem_raw;
-    int64_t* pre = reinterpret_cast<int64_t*>(smem_raw + kWarps * kStages * 2 * kHalf);
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    int64_t* pre = reinterpret_cast<int64_t*>(ring + kWarps * kStages * 2 * kHalf);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, qd = lane & 3;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&s_full[0][0] + i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    uint64_t* full = s_full[warp];
     pdl_wait();
     pdl_trigger();
-    const Line line = make_line(a, pre, s_warp, blockIdx.x == 0);
+    const Line line = make_line(a, pre, s_warp, blockIdx.x == 0);  // its barriers also publish the mbarriers
     const int64_t x1 = min(line.total, (blockIdx.x + 1) * line.share);
     uint8_t* my_ring = ring + warp * (kStages * 2 * kHalf);
     const uint32_t my_ring_u = smem_u32(my_ring);
-    const T* kbase = reinterpret_cast<const T*>(a.c.k);
-    const T* vbase = reinterpret_cast<const T*>(a.c.v);
+    bool ok = true;          // no wait has run out
+    uint32_t loads = 0;      // steps of this warp before the tile's: the ring goes on across tiles
+    // where a lane's rows of a ldmatrix begin within an atom, for its 16 dims 0 .. 3
+    const int mm = lane >> 3, mr = lane & 7;
+    uint32_t k_off[4], v_off[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        k_off[i] = ((mm >> 1) * 8 + mr) * 128 + (((2 * i + (mm & 1)) ^ mr) << 4);
+        v_off[i] = ((mm & 1) * 8 + mr) * 128 + (((2 * i + (mm >> 1)) ^ mr) << 4);
+    }
 
+    if (threadIdx.x == 0) part_join<D>(a)[blockIdx.x].pieces = 0;
     for (int64_t x = blockIdx.x * line.share; x < x1;) {
         const Tile t = find_tile(a, pre, x);
         const int64_t xe = min(x1, t.begin + t.blocks);
@@ -227,8 +255,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
         const int vb0 = static_cast<int>(x - t.begin);
         const int nsteps = max(0, min(static_cast<int>(xe - t.begin), span.blocks) - vb0);  // the same for all warps
         const int32_t* table = a.table + t.b * a.ld_table;
-        const T* kh = kbase + t.head * a.c.sh;
-        const T* vh = vbase + t.head * a.c.sh;
 
         // Queries: fragments of the 16 x D tile, zero rows beyond it.  Lane
         // (g, qd) holds rows g and g + 8, dims 16 kk + 2 qd + {0, 1} and + 8.
@@ -241,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
                 const int row = g + 8 * hh;
                 pos[hh] = t.r.L - t.r.n + (t.row0 + row) / a.G;
                 const bool live = row < t.rows;
-                const T* p = q0 + (live ? row_offset(a, t, row, a.ld_q) : 0) + 2 * qd;
+                const T* p = q0 + (live ? row_offset(a, t.r.start, t.head, t.row0 + row, a.ld_q) : 0) + 2 * qd;
 #pragma unroll
                 for (int kk = 0; kk < kNd; ++kk) {
                     qf[kk][hh] = live ? __ldg(reinterpret_cast<const uint32_t*>(p + kk * 16)) : 0u;
@@ -281,28 +307,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
         // Starts the copies of step s into its stage.  The pages of steps s ..
         // are in `pages` (refilled every 32 steps).
         auto load_step = [&](int s) {
-            if (s < nsteps) {
-                if ((s & 31) == 0) fetch_pages(s);
-                const int page = __shfl_sync(0xffffffffu, pages, s & 31);
+            if (s >= nsteps) return;
+            if ((s & 31) == 0) fetch_pages(s);
+            const int page = __shfl_sync(0xffffffffu, pages, s & 31);
+            const int st = (loads + s) % kStages;
+            lost = page >= 0 ? lost & ~(1u << st) : lost | (1u << st);
+            if (lane == 0) {
+                uint8_t* dst = my_ring + st * (2 * kHalf);
+                if (page < 0) {
+                    mbar_arrive(&full[st]);
+                    return;
+                }
+                mbar_arrive_expect_tx(&full[st], 2 * kHalf);
                 const int key0 = span.block(vb0 + s) * kBlock + warp * kStep;
-                const int64_t base = page >= 0 ? page * a.c.sp + (key0 & (a.c.page_size - 1)) * a.c.st : 0;
-                const uint32_t bit = 1u << (s % kStages);
-                lost = page >= 0 ? lost & ~bit : lost | bit;
-                const uint32_t dst = my_ring_u + (s % kStages) * (2 * kHalf);
+                int c[4] = {0, page, page, page};
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int c = i * 32 + lane;
-                    const int key = c / kChunks, dc = c % kChunks;
-                    const int j = key0 + key;
-                    const bool ok = page >= 0 && j <= span.pmax &&
-                                    (a.window <= 0 || j > span.pmin - a.window || j < a.sinks);
-                    const int64_t off = ok ? base + key * a.c.st + dc * 8 : 0;
-                    const uint32_t d = dst + key * (D * 2) + ((dc ^ (key & 7)) << 4);
-                    cp_async16(d, kh + off, ok);
-                    cp_async16(d + kHalf, vh + off, ok);
+                for (int d = 1; d < 4; ++d) {
+                    if (d == a.d_tok) c[d] = key0 & (a.c.page_size - 1);
+                    if (d == a.d_head) c[d] = t.head;
+                }
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    tma_load_4d(dst + h * kAtom, &tmK, &full[st], h * 64, c[1], c[2], c[3]);
+                    tma_load_4d(dst + kHalf + h * kAtom, &tmV, &full[st], h * 64, c[1], c[2], c[3]);
                 }
             }
-            cp_commit();
         };
 
 #pragma unroll
@@ -310,9 +339,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
         for (int s = 0; s < nsteps; ++s) {
             __syncwarp();  // every lane has read the stage that the next copies overwrite
             load_step(s + kStages - 1);
-            cp_wait<kStages - 1>();
+            const uint32_t n = loads + s, stage = n % kStages;
+            if (ok) ok = mbar_wait(&full[stage], (n / kStages) & 1, a.status, &s_abort);
             __syncwarp();
-            const uint32_t kst = my_ring_u + (s % kStages) * (2 * kHalf);
+            if ((lost >> stage) & 1u) continue;  // no page: nothing of the step is seen
+            uint8_t* sv = my_ring + stage * (2 * kHalf) + kHalf;
+            const uint32_t kst = my_ring_u + stage * (2 * kHalf);
             const uint32_t vst = kst + kHalf;
             const int key0 = span.block(vb0 + s) * kBlock + warp * kStep;
 
@@ -321,20 +353,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[j][e] = 0.0f;
-            {
-                const int mm = lane >> 3, r = lane & 7;
-                const uint32_t krow = kst + ((mm >> 1) * 8 + r) * (D * 2);
 #pragma unroll
-                for (int kk = 0; kk < kNd; ++kk) {
-                    uint32_t b[4];
-                    ldsm4(krow + (((kk * 2 + (mm & 1)) ^ r) << 4), b);
-                    mma16816<T>(sc[0], qf[kk], b[0], b[1]);
-                    mma16816<T>(sc[1], qf[kk], b[2], b[3]);
-                }
+            for (int kk = 0; kk < kNd; ++kk) {
+                uint32_t b[4];
+                ldsm4(kst + (kk >> 2) * kAtom + k_off[kk & 3], b);
+                mma16816<T>(sc[0], qf[kk], b[0], b[1]);
+                mma16816<T>(sc[1], qf[kk], b[2], b[3]);
             }
             // masks, unless every row sees every key of the step
-            const bool no_page = (lost >> (s % kStages)) & 1u;
-            const bool whole = !no_page && key0 + kStep - 1 <= span.pmin &&
+            const bool whole = key0 + kStep - 1 <= span.pmin &&
                                (a.window <= 0 || key0 > span.pmax - a.window || key0 + kStep <= a.sinks);
             // A row that has seen a key has a finite maximum, even if the score
             // was -inf (its result is then 0 / 0, as the formula's), and only
@@ -347,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int key = key0 + j * 8 + 2 * qd + (e & 1);
-                        if (!no_page && paged_sees(key, pos[e >> 1], a.window, a.sinks))
+                        if (paged_sees(key, pos[e >> 1], a.window, a.sinks))
                             low[e >> 1] = -FLT_MAX;
                         else
                             sc[j][e] = -INFINITY;
@@ -390,15 +417,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
             }
             // O += P V
             bool slow = false;
-            if (!whole && i0 != i1) {
-                // Some query sees a key of this step that another one does not:
-                // if such a V holds NaN or an infinity, 0 x V would reach the
-                // queries that must not see it.
+            if (!whole) {
+                // Rows of V that no query of the tile sees become zeros.  If another
+                // one, which some of the queries see and some do not, holds NaN or an
+                // infinity, 0 x V would reach the queries that must not see it.
                 bool nf = false;
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i)
-                    nf |= any_nonfinite<T>(*reinterpret_cast<const uint4*>(my_ring + (s % kStages) * (2 * kHalf) + kHalf + (i * 32 + lane) * 16));
-                slow = __any_sync(0xffffffffu, nf);
+                for (int i = 0; i < kPieces; ++i) {
+                    uint4* piece = reinterpret_cast<uint4*>(sv) + i * 32 + lane;
+                    const int j = key0 + (((i * 32 + lane) >> 3) & (kStep - 1));
+                    if (j <= span.pmax && (a.window <= 0 || j > span.pmin - a.window || j < a.sinks))
+                        nf |= any_nonfinite<T>(*piece);
+                    else
+                        *piece = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_shared();  // before the copies that will overwrite it
+                slow = __any_sync(0xffffffffu, nf) && i0 != i1;
+                __syncwarp();
             }
             if (!slow) {
                 uint32_t pa[4];
@@ -406,17 +441,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
                 pa[1] = pack2_out<T>(p[0][2], p[0][3]);
                 pa[2] = pack2_out<T>(p[1][0], p[1][1]);
                 pa[3] = pack2_out<T>(p[1][2], p[1][3]);
-                const int mm = lane >> 3, r = lane & 7;
-                const uint32_t vrow = vst + ((mm & 1) * 8 + r) * (D * 2);
 #pragma unroll
                 for (int jj = 0; jj < kNd; ++jj) {
                     uint32_t b[4];
-                    ldsm4_t(vrow + (((jj * 2 + (mm >> 1)) ^ r) << 4), b);
+                    ldsm4_t(vst + (jj >> 2) * kAtom + v_off[jj & 3], b);
                     mma16816<T>(o[2 * jj], pa, b[0], b[1]);
                     mma16816<T>(o[2 * jj + 1], pa, b[2], b[3]);
                 }
             } else {
-                const T* vs = reinterpret_cast<const T*>(my_ring + (s % kStages) * (2 * kHalf) + kHalf);
                 for (int key = 0; key < kStep; ++key) {
                     const int src = (lane & ~3) | ((key & 7) >> 1);
 #pragma unroll
@@ -435,13 +467,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
                             for (int j = 0; j < 2 * kNd; ++j)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
-                                    o[j][2 * hh + e] += w * to_f32<T>(vs[key * D + ((j ^ (key & 7)) << 3) + 2 * qd + e]);
+                                    o[j][2 * hh + e] += w * to_f32<T>(*reinterpret_cast<const T*>(
+                                                                sv + (j >> 3) * kAtom + key * 128 + (((j & 7) ^ (key & 7)) << 4) + (2 * qd + e) * 2));
                         }
                     }
                 }
             }
         }
-        cp_wait<0>();
+        loads += nsteps;
         // Join the four warps' keys: rescale to the common maximum, then add.
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -469,6 +502,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
         __syncthreads();
         const bool whole_tile = x == t.begin && xe == t.begin + t.blocks;
         const int slot = x == blockIdx.x * line.share ? 0 : 1;
+        if (threadIdx.x == 0 && x == t.begin && !whole_tile)  // this CTA's last piece: the tile goes on in the next ones
+            part_join<D>(a)[blockIdx.x] = Join{static_cast<int>((t.begin + t.blocks - 1) / line.share) - static_cast<int>(blockIdx.x) + 1,
+                                               slot, t.r.start, t.head, t.row0, t.rows};
         for (int e = threadIdx.x; e < t.rows * (D / 4); e += kThreads) {
             const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
             float mx = s_m[0][row], ls = 0.0f;
@@ -489,51 +525,47 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(PagedAttnAr
                 uint2 w2;
                 w2.x = pack2_out<T>(v.x * inv, v.y * inv);
                 w2.y = pack2_out<T>(v.z * inv, v.w * inv);
-                *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row_offset(a, t, row, a.ld_out) + d4) = w2;
+                *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row_offset(a, t.r.start, t.head, t.row0 + row, a.ld_out) + d4) = w2;
             } else {
                 *reinterpret_cast<float4*>(part_o<D>(a, blockIdx.x, slot) + row * D + d4) = v;
                 if (d4 == 0) part_ml<D>(a, blockIdx.x, slot)[row] = make_float2(mx, ls);
             }
         }
-        __syncthreads();  // the ring is free for the next tile
+        fence_async_shared();  // the exchange, before the copies that overwrite it
+        __syncthreads();       // the ring is free for the next tile
         x = xe;
+    }
+    if (s_abort) {  // a wait ran out: give this CTA's copies in flight time to land
+        const unsigned long long t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
     }
 }
 
-// Joins the pieces of the tile that begins in CTA c's share and ends in a
-// later one's, c = blockIdx.x: out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M).
+// Joins the pieces of the tile in CTA c's record, c = blockIdx.x:
+// out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M).  A tile may have as many
+// pieces as there are CTAs, so the threads that a tile's rows leave over share
+// the pieces.
+constexpr int kJoinThreads = 256;
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) k_paged_join(PagedAttnArgs a) {
-    extern __shared__ int64_t pre[];  // prefix sums, then a weight per row and piece
-    __shared__ int64_t s_warp[kWarps];
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedAttnArgs a) {
+    extern __shared__ float wgt[];  // [pieces][kRows]
     __shared__ float s_inv[kRows];
-    // The lengths were complete before the kernel whose results this one reads
-    // began its work, and this one starts after that: no wait is needed for them.
-    const Line line = make_line(a, pre, s_warp, false);
-    const int64_t end = (blockIdx.x + 1) * line.share;
-    bool cut = end < line.total;
-    Tile t;
-    if (cut) {
-        t = find_tile(a, pre, end - 1);
-        cut = t.begin / line.share == blockIdx.x && t.begin + t.blocks > end;
-    }
+    __shared__ float4 s_sum[kJoinThreads];
     pdl_wait();
     pdl_trigger();
-    if (!cut) return;
-    __syncthreads();  // pre has been read by all
-    const int64_t c0 = blockIdx.x, c1 = (t.begin + t.blocks - 1) / line.share;
-    const int np = static_cast<int>(c1 - c0 + 1);
-    float* wgt = reinterpret_cast<float*>(pre);  // [np][kRows]
-    // the first piece begins at the tile's begin, the others at their CTA's share
-    auto slot_of = [&](int64_t c) { return max(t.begin, c * line.share) == c * line.share ? 0 : 1; };
+    const Join t = part_join<D>(a)[blockIdx.x];
+    if (t.pieces == 0) return;
+    const int64_t c0 = blockIdx.x;
+    const int np = t.pieces;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int row = warp; row < t.rows; row += kWarps) {
+    auto slot_of = [&](int i) { return i == 0 ? t.slot : 0; };
+    for (int row = warp; row < t.rows; row += kJoinThreads / 32) {
         float mx = -INFINITY, ls = 0.0f;
-        for (int i = lane; i < np; i += 32) mx = fmaxf(mx, part_ml<D>(a, c0 + i, slot_of(c0 + i))[row].x);
+        for (int i = lane; i < np; i += 32) mx = fmaxf(mx, part_ml<D>(a, c0 + i, slot_of(i))[row].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         for (int i = lane; i < np; i += 32) {
-            const float2 ml = part_ml<D>(a, c0 + i, slot_of(c0 + i))[row];
+            const float2 ml = part_ml<D>(a, c0 + i, slot_of(i))[row];
             const float f = ml.x == mx ? 1.0f : ex2((ml.x - mx) * a.qscale);
             wgt[i * kRows + row] = f;
             ls += ml.y * f;
@@ -543,44 +575,67 @@ __global__ void __launch_bounds__(kThreads) k_paged_join(PagedAttnArgs a) {
         if (lane == 0) s_inv[row] = mx == -INFINITY ? 0.0f : 1.0f / ls;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < t.rows * (D / 4); e += kThreads) {
+    // four dims of a row per thread; `groups` threads share its pieces
+    const int items = t.rows * (D / 4);
+    const int groups = max(1, kJoinThreads / items);
+    for (int e0 = 0; e0 < items; e0 += kJoinThreads) {
+        const int e = groups > 1 ? static_cast<int>(threadIdx.x) % items : e0 + static_cast<int>(threadIdx.x);
+        const int g = groups > 1 ? static_cast<int>(threadIdx.x) / items : 0;
         const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
         float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-        for (int i = 0; i < np; ++i) {
-            const float f = wgt[i * kRows + row];
-            const float4 y = *reinterpret_cast<const float4*>(part_o<D>(a, c0 + i, slot_of(c0 + i)) + row * D + d4);
-            v.x = fmaf(y.x, f, v.x);
-            v.y = fmaf(y.y, f, v.y);
-            v.z = fmaf(y.z, f, v.z);
-            v.w = fmaf(y.w, f, v.w);
+        if (g < groups && e < items) {
+#pragma unroll 8
+            for (int i = g; i < np; i += groups) {
+                const float f = wgt[i * kRows + row];
+                const float4 y = *reinterpret_cast<const float4*>(part_o<D>(a, c0 + i, slot_of(i)) + row * D + d4);
+                v.x = fmaf(y.x, f, v.x);
+                v.y = fmaf(y.y, f, v.y);
+                v.z = fmaf(y.z, f, v.z);
+                v.w = fmaf(y.w, f, v.w);
+            }
         }
-        const float inv = s_inv[row];
-        uint2 w2;
-        w2.x = pack2_out<T>(v.x * inv, v.y * inv);
-        w2.y = pack2_out<T>(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row_offset(a, t, row, a.ld_out) + d4) = w2;
+        if (groups > 1) {
+            s_sum[threadIdx.x] = v;
+            __syncthreads();
+            if (g == 0)
+                for (int i = 1; i < groups; ++i) {
+                    const float4 y = s_sum[i * items + e];
+                    v.x += y.x;
+                    v.y += y.y;
+                    v.z += y.z;
+                    v.w += y.w;
+                }
+        }
+        if (g == 0 && e < items) {
+            const float inv = s_inv[row];
+            uint2 w2;
+            w2.x = pack2_out<T>(v.x * inv, v.y * inv);
+            w2.y = pack2_out<T>(v.z * inv, v.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row_offset(a, t.start, t.head, t.row0 + row, a.ld_out) + d4) = w2;
+        }
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_t(PagedAttnArgs a, int num_sms, cudaStream_t st) {
     a.grid = kCtasPerSm * num_sms;
-    const int ring = kWarps * kStages * 2 * kStep * D * 2;
+    CUtensorMap tmK, tmV;
+    if (!paged_cache_maps(a.c, kStep, &tmK, &tmV, &a.d_tok, &a.d_head)) return cudaErrorInvalidValue;
+    const int ring = 1024 + kWarps * kStages * 2 * kStep * D * 2;
     const int pre = (a.B + 1) * 8;
     auto kern = k_paged_attn<T, D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + pre);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(a.grid), dim3(kThreads), ring + pre, st, a);
+    e = launch_pdl(kern, dim3(a.grid), dim3(kThreads), ring + pre, st, tmK, tmV, a);
     if (e != cudaSuccess) return e;
     const int wgt = a.grid * kRows * 4;
-    return launch_pdl(k_paged_join<T, D>, dim3(a.grid), dim3(kThreads), std::max(pre, wgt), st, a);
+    return launch_pdl(k_paged_join<T, D>, dim3(a.grid), dim3(kJoinThreads), wgt, st, a);
 }
 
 }  // namespace
 
 size_t paged_rows16_bytes(int D, int num_sms) {
-    return static_cast<size_t>(kCtasPerSm) * num_sms * 2 * kRows * (D + 2) * 4;
+    return static_cast<size_t>(kCtasPerSm) * num_sms * (2 * kRows * (D + 2) * 4 + sizeof(Join));
 }
 
 cudaError_t launch_paged_rows16(PagedAttnArgs a, int num_sms, cudaStream_t st) {

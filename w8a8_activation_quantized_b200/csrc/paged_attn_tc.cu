@@ -81,7 +81,6 @@ struct TcArgs {
     int tok;              // tokens per 128-row tile: 128 / G
     int boxes;            // pages per block (at least 1)
     int box_keys;         // keys per box: min(page_size, 128)
-    int d_tok, d_head;    // which of the map's outer dimensions (1..3) is the token, the head; the page is the third
     int grid;
     TcPlan* plan;
     TcUnit* units;
@@ -338,15 +337,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
-                                            int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
-
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -594,8 +584,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                             int c[4] = {half * 64, pg, pg, pg};
 #pragma unroll
                             for (int d = 1; d < 4; ++d) {
-                                if (d == t.d_tok) c[d] = in_page;
-                                if (d == t.d_head) c[d] = head;
+                                if (d == a.d_tok) c[d] = in_page;
+                                if (d == a.d_head) c[d] = head;
                             }
                             tma_load_4d(sRing + s * TB + half * AB + box * t.box_keys * 128, map, &full[s], c[0], c[1], c[2], c[3]);
                         }
@@ -1052,28 +1042,10 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
     t.ranges = reinterpret_cast<int2*>(ws + l.ranges);
     t.part = reinterpret_cast<float*>(ws + l.part);
 
-    // Cache maps: dims {D, then token, head and page by ascending stride}.
-    struct Dim {
-        int64_t n, stride;
-        int id;
-    } dim[3] = {{p.c.page_size, p.c.st, 0}, {p.c.H_kv, p.c.H_kv > 1 ? p.c.sh : 0, 1}, {p.c.num_pages, p.c.num_pages > 1 ? p.c.sp : 0, 2}};
-    std::stable_sort(dim, dim + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D)}, strides[3];
-    cuuint32_t box[4] = {64, 1, 1, 1}, ones[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 3; ++i) {
-        dims[i + 1] = dim[i].n;
-        strides[i] = std::max<int64_t>(dim[i].stride, D) * 2;  // a dimension of one element: any stride
-        if (dim[i].id == 0) {
-            t.d_tok = i + 1;
-            box[i + 1] = t.box_keys;
-        }
-        if (dim[i].id == 1) t.d_head = i + 1;
-    }
-    const auto type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap tmQ, tmK, tmV;
-    if (!encode_tensor_map(&tmK, type, 4, p.c.k, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tensor_map(&tmV, type, 4, p.c.v, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
+    if (!paged_cache_maps(p.c, t.box_keys, &tmK, &tmV, &t.p.d_tok, &t.p.d_head)) return cudaErrorInvalidValue;
+    const auto type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint32_t ones[3] = {1, 1, 1};
     const cuuint64_t qd[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.H_q), static_cast<cuuint64_t>(p.T)};
     const cuuint64_t qs[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(p.ld_q) * 2};
     const cuuint32_t qb[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(t.tok)};

@@ -3,6 +3,8 @@
 // prefix sums over the requests.
 #pragma once
 
+#include <algorithm>
+
 #include "cider_device.cuh"
 #include "paged.h"
 
@@ -49,6 +51,41 @@ struct PagedSpan {
 
 __device__ __forceinline__ bool paged_sees(int key, int pos, int window, int sinks) {
     return key <= pos && (window <= 0 || key > pos - window || key < sinks);
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Tensor maps of K and V for boxes of 64 dims x box_keys keys of one head and
+// page (128-byte swizzle).  Dimension 0 is D; the token, the head and the page
+// follow by ascending stride, the first two at *d_tok and *d_head.
+inline bool paged_cache_maps(const PagedCache& c, int box_keys, CUtensorMap* tmK, CUtensorMap* tmV, int* d_tok, int* d_head) {
+    struct Dim {
+        int64_t n, stride;
+        int id;
+    } dim[3] = {{c.page_size, c.st, 0}, {c.H_kv, c.sh, 1}, {c.num_pages, c.sp, 2}};
+    std::stable_sort(dim, dim + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D)}, strides[3];
+    cuuint32_t box[4] = {64, 1, 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        dims[i + 1] = dim[i].n;
+        strides[i] = std::max<int64_t>(dim[i].stride, c.D) * 2;  // a dimension of one element (stride 0): any will do
+        if (dim[i].id == 0) {
+            *d_tok = i + 1;
+            box[i + 1] = box_keys;
+        }
+        if (dim[i].id == 1) *d_head = i + 1;
+    }
+    const auto type = c.dt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return encode_tensor_map(tmK, type, 4, c.k, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           encode_tensor_map(tmV, type, 4, c.v, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Exclusive prefix sum of a value per thread; `total` gets the sum.  s_warp:
