@@ -14,15 +14,16 @@
 // tensor pipe far from its rate: HBM is the bound, and the 128-row tiles of
 // tcgen05 would only add latency.
 //
-// Loads: each warp has its own ring of kStages steps (16 keys of K and of V) in
-// shared memory, filled by TMA in boxes of 16 keys x 64 dims (128-byte swizzle,
-// one mbarrier per stage), so warps never wait for one another within a tile;
-// two CTAs of four warps per SM keep up to 2 x 4 x 3 x 8 KB = 192 KB in flight.
-// (With 16-byte cp.async in their place the loads took half of the kernel's
-// instructions: four requests of up to 32K keys 38.7 us, with TMA see below.)
-// Pages that no query of the tile sees are not read.  Where only some keys of a
-// step are seen by any query, the other rows of V are zeroed in shared memory:
-// what the cache's unwritten slots hold may be NaN, and 0 x NaN is not 0.
+// Loads: a fifth warp copies 64-key blocks of K and V (TMA, 128-byte swizzle,
+// one box per page and 64 dims) into a ring of 96 KB, ahead of the four warps
+// that use them, each 16 keys of a block, and on into the next tile; two CTAs
+// per SM keep up to 192 KB in flight.  (The using warps' instructions set the
+// pace where the bytes do not: with 16-byte cp.async of their own, and with TMA
+// of their own, four requests of up to 32K keys took 49.5 and 45.2 us.)  Pages that
+// no query of the tile sees are not read; their boxes lie outside the tensor
+// map, which makes them zeros.  Where only some keys of a step are seen by any
+// query, the other rows of V are zeroed in shared memory: what the cache's
+// unwritten slots hold may be NaN, and 0 x NaN is not 0.
 //
 // Split: the work of the whole batch is one line of blocks of 64 keys -- per
 // request, per 16-row tile, per KV head, its blocks -- cut into equal pieces,
@@ -47,10 +48,12 @@ namespace {
 
 constexpr int kRows = 16;      // rows of a tile (mma M)
 constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kUsers = kWarps * 32;       // threads of the warps that compute; one more warp loads
+constexpr int kThreads = kUsers + 32;
 constexpr int kStep = 16;      // keys per warp and step
 constexpr int kBlock = kWarps * kStep;  // keys per block of the line
-constexpr int kStages = 3;
+template <int D>
+constexpr int kRing = D == 128 ? 3 : 6;  // blocks in the ring: 96 KB
 constexpr int kCtasPerSm = 2;
 // Shortest share of a CTA, in blocks: below it the pieces' join costs more
 // than the parallelism gains.
@@ -76,6 +79,22 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
 }
 
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Barrier of the warps that compute.
+__device__ __forceinline__ void users_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kUsers) : "memory"); }
+
+__device__ __forceinline__ bool users_or(bool x) {  // true if any thread passes true
+    uint32_t y;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(y)
+        : "r"(static_cast<uint32_t>(x)), "n"(kUsers)
+        : "memory");
+    return y != 0;
+}
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -148,7 +167,7 @@ __device__ __forceinline__ Line make_line(const PagedAttnArgs& a, int64_t* pre, 
     for (int b = b0; b < b1; ++b) pre[b] += base;
     if (threadIdx.x == 0) pre[a.B] = line.total;
     __syncthreads();
-    line.share = max(static_cast<int64_t>(kMinShare), (line.total + a.grid - 1) / a.grid);
+    line.share = max(static_cast<int64_t>(kMinShare), div_nonneg(line.total + a.grid - 1, a.grid));
     return line;
 }
 
@@ -166,13 +185,23 @@ __device__ __forceinline__ Tile find_tile(const PagedAttnArgs& a, const int64_t*
     int tiles;
     t.r = paged_request(a, t.b, &bad);
     request_blocks(a, t.r, &tiles, &t.blocks);
-    const int64_t u = (x - pre[t.b]) / t.blocks;  // tile * H_kv + head
+    const int64_t u = div_nonneg(x - pre[t.b], t.blocks);  // tile * H_kv + head
     t.begin = pre[t.b] + u * t.blocks;
-    t.head = static_cast<int>(u % a.c.H_kv);
-    t.row0 = static_cast<int>(u / a.c.H_kv) * kRows;
+    const int tile = static_cast<int>(div_nonneg(u, a.c.H_kv));
+    t.head = static_cast<int>(u - static_cast<int64_t>(tile) * a.c.H_kv);
+    t.row0 = tile * kRows;
     t.rows = min(kRows, t.r.n * a.G - t.row0);
     return t;
 }
+
+// A piece of a tile that a CTA computes: found, with its queries, by the warp that
+// loads, while the others are busy with the one before.
+struct Piece {
+    Tile t;
+    PagedSpan<kBlock> span;
+    int vb0, vb1;  // its blocks of the span; vb1 < 0: no more pieces
+    int slot;      // of its partial result; -1: it is the whole tile
+};
 
 // Element offset of a request's (token, head) row f in q (at ld) or out.
 __device__ __forceinline__ int64_t row_offset(const PagedAttnArgs& a, int start, int head, int f, int64_t ld) {
@@ -207,333 +236,385 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __grid_constant__ CUtensorMap tmK,
                                                                      const __grid_constant__ CUtensorMap tmV,
                                                                      const __grid_constant__ PagedAttnArgs a) {
-    constexpr int kHalf = kStep * D * 2;                 // bytes of K (or V) of one step
-    constexpr int kAtom = kStep * 128;                   // bytes of 64 dims of it
+    constexpr int kStages = kRing<D>;
+    constexpr int kAtom = kBlock * 128;                  // bytes of 64 dims of a block
+    constexpr int kHalf = kBlock * D * 2;                // bytes of K (or V) of a block
     constexpr int kPieces = kStep * (D / 8) / 32;        // 16-byte pieces of V per lane and step
     constexpr int kNd = D / 16;                          // d-steps of 16
+    static_assert(kWarps * kRows * D * 4 <= 2 * kHalf, "the warps' exchange fits one stage");
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_full[kWarps][kStages];
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ uint32_t s_lost[kStages];                 // per 16 keys of a block: the page is missing
     __shared__ int s_abort;
-    __shared__ int64_t s_warp[kWarps];
+    __shared__ int64_t s_warp[kThreads / 32];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ Piece s_piece[2];
+    __shared__ __align__(128) uint4 s_q[2][D / 64][kRows][8];  // queries of a piece: [64 dims][row][8 dims]
+    __shared__ uint64_t piece_full[2], piece_empty[2];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int64_t* pre = reinterpret_cast<int64_t*>(ring + kWarps * kStages * 2 * kHalf);
+    int64_t* pre = reinterpret_cast<int64_t*>(ring + kStages * 2 * kHalf);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, qd = lane & 3;
     if (threadIdx.x == 0) {
         s_abort = 0;
-        for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&s_full[0][0] + i, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&piece_full[i], 1);
+            mbar_init(&piece_empty[i], 1);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    uint64_t* full = s_full[warp];
     pdl_wait();
     pdl_trigger();
     const Line line = make_line(a, pre, s_warp, blockIdx.x == 0);  // its barriers also publish the mbarriers
     const int64_t x1 = min(line.total, (blockIdx.x + 1) * line.share);
-    uint8_t* my_ring = ring + warp * (kStages * 2 * kHalf);
-    const uint32_t my_ring_u = smem_u32(my_ring);
-    bool ok = true;          // no wait has run out
-    uint32_t loads = 0;      // steps of this warp before the tile's: the ring goes on across tiles
-    // where a lane's rows of a ldmatrix begin within an atom, for its 16 dims 0 .. 3
-    const int mm = lane >> 3, mr = lane & 7;
-    uint32_t k_off[4], v_off[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        k_off[i] = ((mm >> 1) * 8 + mr) * 128 + (((2 * i + (mm & 1)) ^ mr) << 4);
-        v_off[i] = ((mm & 1) * 8 + mr) * 128 + (((2 * i + (mm >> 1)) ^ mr) << 4);
-    }
+    bool ok = true;      // false: a wait has run out, and no other one is begun
+    uint32_t blk = 0;    // blocks of the ring so far
 
-    if (threadIdx.x == 0) part_join<D>(a)[blockIdx.x].pieces = 0;
-    for (int64_t x = blockIdx.x * line.share; x < x1;) {
-        const Tile t = find_tile(a, pre, x);
-        const int64_t xe = min(x1, t.begin + t.blocks);
-        PagedSpan<kBlock> span;
-        const int i0 = t.row0 / a.G, i1 = (t.row0 + t.rows - 1) / a.G;
-        span.set(t.r.L - t.r.n + i0, t.r.L - t.r.n + i1, a.window, a.sinks);
-        const int vb0 = static_cast<int>(x - t.begin);
-        const int nsteps = max(0, min(static_cast<int>(xe - t.begin), span.blocks) - vb0);  // the same for all warps
-        const int32_t* table = a.table + t.b * a.ld_table;
-
-        // Queries: fragments of the 16 x D tile, zero rows beyond it.  Lane
-        // (g, qd) holds rows g and g + 8, dims 16 kk + 2 qd + {0, 1} and + 8.
-        uint32_t qf[kNd][4];
-        int pos[2];
-        {
-            const T* q0 = static_cast<const T*>(a.q);
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int row = g + 8 * hh;
-                pos[hh] = t.r.L - t.r.n + (t.row0 + row) / a.G;
-                const bool live = row < t.rows;
-                const T* p = q0 + (live ? row_offset(a, t.r.start, t.head, t.row0 + row, a.ld_q) : 0) + 2 * qd;
-#pragma unroll
-                for (int kk = 0; kk < kNd; ++kk) {
-                    qf[kk][hh] = live ? __ldg(reinterpret_cast<const uint32_t*>(p + kk * 16)) : 0u;
-                    qf[kk][2 + hh] = live ? __ldg(reinterpret_cast<const uint32_t*>(p + kk * 16 + 8)) : 0u;
+    if (warp == kWarps) {
+        // ------------------------------- loads -------------------------------
+        const int box_keys = min(a.c.page_size, kBlock), boxes = kBlock / box_keys;  // 1, 2 or 4 pages per block
+        const int box = lane % boxes, half = (lane / boxes) % (D / 64), kv = lane / boxes / (D / 64);
+        if (lane == 0) part_join<D>(a)[blockIdx.x].pieces = 0;
+        int64_t x = blockIdx.x * line.share;
+        for (int n = 0; ok; ++n) {
+            const int buf = n & 1;
+            ok = mbar_wait(&piece_empty[buf], ((n >> 1) & 1) ^ 1, a.status, &s_abort);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (x >= x1) {  // no more pieces
+                if (lane == 0) {
+                    s_piece[buf].vb1 = -1;
+                    mbar_arrive(&piece_full[buf]);
                 }
+                break;
             }
-        }
-
-        float o[2 * kNd][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 2 * kNd; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-
-        // Page numbers of 32 steps of this warp, one per lane; -1: none, or one
-        // that the cache does not have.  `lost`: a bit per stage of the ring
-        // whose step has no page.
-        int pages = -1;
-        uint32_t lost = 0;
-        auto fetch_pages = [&](int s) {
-            pages = -1;
-            if (s + lane < nsteps) {
-                const int key0 = span.block(vb0 + s + lane) * kBlock + warp * kStep;
-                if (key0 < t.r.L) {
-                    const int e = key0 >> a.c.ps_log2;  // < width, because L <= width * page_size
-                    const bool used = key0 <= span.pmax && (a.window <= 0 || key0 + kStep - 1 > span.pmin - a.window || key0 < a.sinks);
-                    if (used) {
-                        const int p = __ldg(table + e);
-                        if (p >= 0 && p < a.c.num_pages)
-                            pages = p;
-                        else
-                            atomicOr(a.status, kStatusIndex);
-                    }
-                }
-            }
-        };
-        // Starts the copies of step s into its stage.  The pages of steps s ..
-        // are in `pages` (refilled every 32 steps).
-        auto load_step = [&](int s) {
-            if (s >= nsteps) return;
-            if ((s & 31) == 0) fetch_pages(s);
-            const int page = __shfl_sync(0xffffffffu, pages, s & 31);
-            const int st = (loads + s) % kStages;
-            lost = page >= 0 ? lost & ~(1u << st) : lost | (1u << st);
-            if (lane == 0) {
-                uint8_t* dst = my_ring + st * (2 * kHalf);
-                if (page < 0) {
-                    mbar_arrive(&full[st]);
-                    return;
-                }
-                mbar_arrive_expect_tx(&full[st], 2 * kHalf);
-                const int key0 = span.block(vb0 + s) * kBlock + warp * kStep;
-                int c[4] = {0, page, page, page};
-#pragma unroll
-                for (int d = 1; d < 4; ++d) {
-                    if (d == a.d_tok) c[d] = key0 & (a.c.page_size - 1);
-                    if (d == a.d_head) c[d] = t.head;
-                }
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    tma_load_4d(dst + h * kAtom, &tmK, &full[st], h * 64, c[1], c[2], c[3]);
-                    tma_load_4d(dst + kHalf + h * kAtom, &tmV, &full[st], h * 64, c[1], c[2], c[3]);
-                }
-            }
-        };
-
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) load_step(s);
-        for (int s = 0; s < nsteps; ++s) {
-            __syncwarp();  // every lane has read the stage that the next copies overwrite
-            load_step(s + kStages - 1);
-            const uint32_t n = loads + s, stage = n % kStages;
-            if (ok) ok = mbar_wait(&full[stage], (n / kStages) & 1, a.status, &s_abort);
-            __syncwarp();
-            if ((lost >> stage) & 1u) continue;  // no page: nothing of the step is seen
-            uint8_t* sv = my_ring + stage * (2 * kHalf) + kHalf;
-            const uint32_t kst = my_ring_u + stage * (2 * kHalf);
-            const uint32_t vst = kst + kHalf;
-            const int key0 = span.block(vb0 + s) * kBlock + warp * kStep;
-
-            float sc[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[j][e] = 0.0f;
-#pragma unroll
-            for (int kk = 0; kk < kNd; ++kk) {
-                uint32_t b[4];
-                ldsm4(kst + (kk >> 2) * kAtom + k_off[kk & 3], b);
-                mma16816<T>(sc[0], qf[kk], b[0], b[1]);
-                mma16816<T>(sc[1], qf[kk], b[2], b[3]);
-            }
-            // masks, unless every row sees every key of the step
-            const bool whole = key0 + kStep - 1 <= span.pmin &&
-                               (a.window <= 0 || key0 > span.pmax - a.window || key0 + kStep <= a.sinks);
-            // A row that has seen a key has a finite maximum, even if the score
-            // was -inf (its result is then 0 / 0, as the formula's), and only
-            // one that has seen none keeps -inf (its result is 0).
-            float low[2] = {-FLT_MAX, -FLT_MAX};
-            if (!whole) {
-                low[0] = low[1] = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + j * 8 + 2 * qd + (e & 1);
-                        if (paged_sees(key, pos[e >> 1], a.window, a.sinks))
-                            low[e >> 1] = -FLT_MAX;
-                        else
-                            sc[j][e] = -INFINITY;
-                    }
-            }
-            // running maximum, weights
-            float mn[2];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                float x0 = fmaxf(fmaxf(sc[0][2 * hh], sc[0][2 * hh + 1]), fmaxf(sc[1][2 * hh], sc[1][2 * hh + 1]));
-                x0 = fmaxf(x0, low[hh]);
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-                mn[hh] = fmaxf(m[hh], x0);
-            }
-            if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const float f = mn[hh] == m[hh] ? 1.0f : ex2((m[hh] - mn[hh]) * a.qscale);  // first keys: 2^-inf = 0
-                    l[hh] *= f;
-                    m[hh] = mn[hh];
-#pragma unroll
-                    for (int j = 0; j < 2 * kNd; ++j) {
-                        o[j][2 * hh] *= f;
-                        o[j][2 * hh + 1] *= f;
-                    }
-                }
-            }
-            float p[2][4];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const float ms = (m[hh] == -INFINITY ? 0.0f : m[hh]) * a.qscale - kPOff<T>;  // nothing seen yet: all p = 0
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        p[j][2 * hh + e] = ex2(fmaf(sc[j][2 * hh + e], a.qscale, -ms));
-                        l[hh] += p[j][2 * hh + e];
-                    }
-            }
-            // O += P V
-            bool slow = false;
-            if (!whole) {
-                // Rows of V that no query of the tile sees become zeros.  If another
-                // one, which some of the queries see and some do not, holds NaN or an
-                // infinity, 0 x V would reach the queries that must not see it.
-                bool nf = false;
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    uint4* piece = reinterpret_cast<uint4*>(sv) + i * 32 + lane;
-                    const int j = key0 + (((i * 32 + lane) >> 3) & (kStep - 1));
-                    if (j <= span.pmax && (a.window <= 0 || j > span.pmin - a.window || j < a.sinks))
-                        nf |= any_nonfinite<T>(*piece);
+            const Tile t = find_tile(a, pre, x);
+            const int64_t xe = min(x1, t.begin + t.blocks);
+            PagedSpan<kBlock> span;
+            span.set(t.r.L - t.r.n + t.row0 / a.G, t.r.L - t.r.n + (t.row0 + t.rows - 1) / a.G, a.window, a.sinks);
+            const int vb0 = static_cast<int>(x - t.begin), vb1 = min(static_cast<int>(xe - t.begin), span.blocks);
+            const int32_t* table = a.table + t.b * a.ld_table;
+            // The page numbers of 32 / boxes blocks from vb on, one per lane, and a
+            // bit per lane whose page is missing.
+            int pages = 0;
+            uint32_t bad = 0;
+            auto fetch_pages = [&](int vb) {
+                pages = a.c.num_pages;  // outside the map
+                bool missing = false;
+                const int b = vb + lane / boxes;
+                const int key0 = b < vb1 ? span.block(b) * kBlock + box * box_keys : INT_MAX;
+                // (below L <= width * page_size, because pmax is)
+                if (key0 <= span.pmax && (a.window <= 0 || key0 + box_keys - 1 > span.pmin - a.window || key0 < a.sinks)) {
+                    const int p = __ldg(table + (key0 >> a.c.ps_log2));
+                    if (p >= 0 && p < a.c.num_pages)
+                        pages = p;
                     else
-                        *piece = make_uint4(0, 0, 0, 0);
+                        missing = true;
                 }
-                fence_async_shared();  // before the copies that will overwrite it
-                slow = __any_sync(0xffffffffu, nf) && i0 != i1;
+                if (missing) atomicOr(a.status, kStatusIndex);
+                bad = __ballot_sync(0xffffffffu, missing);
+            };
+            // the piece and its queries, zero rows beyond the tile's
+            {
+                constexpr int kQ = kRows * (D / 8) / 32;
+                uint4 q[kQ];
+#pragma unroll
+                for (int i = 0; i < kQ; ++i) {
+                    const int e = i * 32 + lane, row = e / (D / 8);
+                    q[i] = make_uint4(0, 0, 0, 0);
+                    if (row < t.rows)
+                        q[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row_offset(a, t.r.start, t.head, t.row0 + row, a.ld_q)) + e % (D / 8));
+                }
+                fetch_pages(vb0);
+#pragma unroll
+                for (int i = 0; i < kQ; ++i) {
+                    const int e = i * 32 + lane, row = e / (D / 8), c = e % (D / 8);
+                    s_q[buf][c >> 3][row][(c & 7) ^ (row & 7)] = q[i];
+                }
+                if (lane == 0) {
+                    const int slot = x == t.begin && xe == t.begin + t.blocks ? -1 : x == blockIdx.x * line.share ? 0 : 1;
+                    s_piece[buf] = Piece{t, span, vb0, vb1, slot};
+                    if (slot >= 0 && x == t.begin)  // this CTA's last piece: the tile goes on in the next ones
+                        part_join<D>(a)[blockIdx.x] = Join{static_cast<int>(div_nonneg(t.begin + t.blocks - 1, line.share)) - static_cast<int>(blockIdx.x) + 1,
+                                                           slot, t.r.start, t.head, t.row0, t.rows};
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&piece_full[buf]);
+            }
+            for (int vb = vb0; vb < vb1; ++vb, ++blk) {
+                const int in_batch = (vb - vb0) % (32 / boxes);
+                if (in_batch == 0 && vb > vb0) fetch_pages(vb);
+                const int page = __shfl_sync(0xffffffffu, pages, in_batch * boxes + box);
+                const int st = blk % kStages;
+                if (ok) ok = mbar_wait(&empty[st], ((blk / kStages) & 1) ^ 1, a.status, &s_abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    uint32_t lost = 0;
+                    if (bad)
+                        for (int w = 0; w < kWarps; ++w) lost |= ((bad >> (in_batch * boxes + w * boxes / kWarps)) & 1u) << w;
+                    s_lost[st] = lost;
+                    mbar_arrive_expect_tx(&full[st], 2 * kHalf);
+                }
+                __syncwarp();
+                if (kv < 2) {
+                    int c[4] = {0, page, page, page};
+#pragma unroll
+                    for (int d = 1; d < 4; ++d) {
+                        if (d == a.d_tok) c[d] = (span.block(vb) * kBlock) & (a.c.page_size - 1);
+                        if (d == a.d_head) c[d] = t.head;
+                    }
+                    tma_load_4d(ring + st * (2 * kHalf) + kv * kHalf + half * kAtom + box * box_keys * 128, kv ? &tmV : &tmK, &full[st],
+                                half * 64, c[1], c[2], c[3]);
+                }
                 __syncwarp();
             }
-            if (!slow) {
-                uint32_t pa[4];
-                pa[0] = pack2_out<T>(p[0][0], p[0][1]);
-                pa[1] = pack2_out<T>(p[0][2], p[0][3]);
-                pa[2] = pack2_out<T>(p[1][0], p[1][1]);
-                pa[3] = pack2_out<T>(p[1][2], p[1][3]);
+            x = xe;
+        }
+    } else {
+        // ------------------------------ products ------------------------------
+        const int g = lane >> 2, qd = lane & 3;
+        // Where a lane's row of a ldmatrix begins in a stage, for the first 16 dims
+        // of an atom; the swizzle turns the i-th 16 dims into an exclusive or.
+        const int mm = lane >> 3, mr = lane & 7;
+        const uint32_t k_off = warp * (kStep * 128) + ((mm >> 1) * 8 + mr) * 128 + (((mm & 1) ^ mr) << 4);
+        const uint32_t q_off = ((mm & 1) * 8 + mr) * 128 + (((mm >> 1) ^ mr) << 4);
+        const uint32_t v_off = kHalf + warp * (kStep * 128) + ((mm & 1) * 8 + mr) * 128 + (((mm >> 1) ^ mr) << 4);
+        for (int n = 0;; ++n) {
+            const int buf = n & 1;
+            if (ok) ok = mbar_wait(&piece_full[buf], (n >> 1) & 1, a.status, &s_abort);
+            if (users_or(!ok)) break;  // all go on, or none
+            const PagedSpan<kBlock> span = s_piece[buf].span;
+            const int vb0 = s_piece[buf].vb0, vb1 = s_piece[buf].vb1;
+            if (vb1 < 0) break;
+            int pos[2];
+            {
+                const Tile t = s_piece[buf].t;
 #pragma unroll
-                for (int jj = 0; jj < kNd; ++jj) {
+                for (int hh = 0; hh < 2; ++hh) pos[hh] = t.r.L - t.r.n + (t.row0 + g + 8 * hh) / a.G;
+            }
+            // The queries stay in shared memory at D = 128: in registers, 32, they
+            // would spill others (four requests of up to 32K keys: 49.0 -> 46.3 us).
+            const uint32_t q_row = smem_u32(s_q[buf]) + q_off;
+            uint32_t q[kNd][4];
+            if (D == 64)
+#pragma unroll
+                for (int kk = 0; kk < kNd; ++kk) ldsm4(q_row ^ ((kk & 3) << 5), q[kk]);
+
+            float o[2 * kNd][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 2 * kNd; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+
+            for (int vb = vb0; vb < vb1; ++vb, ++blk) {
+                const int st = blk % kStages;
+                if (ok) ok = mbar_wait(&full[st], (blk / kStages) & 1, a.status, &s_abort);
+                __syncwarp();
+                const uint32_t stage = smem_u32(ring) + st * (2 * kHalf);
+                const int key0 = span.block(vb) * kBlock + warp * kStep;
+                const bool lost = (s_lost[st] >> warp) & 1u;
+
+                float sa[2][4], sc[2][4];  // two chains of products each
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sa[j][e] = sc[j][e] = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < kNd; ++kk) {
                     uint32_t b[4];
-                    ldsm4_t(vst + (jj >> 2) * kAtom + v_off[jj & 3], b);
-                    mma16816<T>(o[2 * jj], pa, b[0], b[1]);
-                    mma16816<T>(o[2 * jj + 1], pa, b[2], b[3]);
+                    if (D != 64) ldsm4((q_row ^ ((kk & 3) << 5)) + (kk >> 2) * (kRows * 128), q[kk]);
+                    ldsm4(((stage + k_off) ^ ((kk & 3) << 5)) + (kk >> 2) * kAtom, b);
+                    mma16816<T>(kk & 1 ? sa[0] : sc[0], q[kk], b[0], b[1]);
+                    mma16816<T>(kk & 1 ? sa[1] : sc[1], q[kk], b[2], b[3]);
                 }
-            } else {
-                for (int key = 0; key < kStep; ++key) {
-                    const int src = (lane & ~3) | ((key & 7) >> 1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[j][e] += sa[j][e];
+                // Masks, unless every row sees every key of the step.  A row that has
+                // seen a key has a finite maximum, even if the score was -inf (its
+                // result is then 0 / 0, as the formula's), and only one that has seen
+                // none keeps -inf (its result is 0).
+                float low[2] = {-FLT_MAX, -FLT_MAX};
+                const bool whole = !lost && key0 + kStep - 1 <= span.pmin &&
+                                   (a.window <= 0 || key0 > span.pmax - a.window || key0 + kStep <= a.sinks);
+                bool slow = false;
+                if (!whole) {
+                    low[0] = low[1] = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + j * 8 + 2 * qd + (e & 1);
+                            if (!lost && paged_sees(key, pos[e >> 1], a.window, a.sinks))
+                                low[e >> 1] = -FLT_MAX;
+                            else
+                                sc[j][e] = -INFINITY;
+                        }
+                    // Rows of V that no query of the tile sees become zeros.  If another
+                    // one, which some of the queries see and some do not, holds NaN or an
+                    // infinity, 0 x V would reach the queries that must not see it.
+                    bool nf = false;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int e = i * 32 + lane, row = (e >> 3) & (kStep - 1);
+                        uint4* piece = reinterpret_cast<uint4*>(ring + st * (2 * kHalf) + kHalf + (e >> 7) * kAtom + (warp * kStep + row) * 128) + (e & 7);
+                        const int j = key0 + row;
+                        if (j <= span.pmax && (a.window <= 0 || j > span.pmin - a.window || j < a.sinks))
+                            nf |= any_nonfinite<T>(*piece);
+                        else
+                            *piece = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_shared();  // before the copies that will overwrite it
+                    slow = __any_sync(0xffffffffu, nf) && span.pmin != span.pmax;
+                    __syncwarp();
+                }
+                // running maximum, weights
+                float mn[2];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    float y = fmaxf(fmaxf(sc[0][2 * hh], sc[0][2 * hh + 1]), fmaxf(sc[1][2 * hh], sc[1][2 * hh + 1]));
+                    y = fmaxf(y, low[hh]);
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                    mn[hh] = fmaxf(m[hh], y);
+                }
+                if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        // p of (row, key): tile key / 8, element key % 2, of lane src
-                        float w = 0.0f;
+                        const float f = mn[hh] == m[hh] ? 1.0f : ex2((m[hh] - mn[hh]) * a.qscale);  // first keys: 2^-inf = 0
+                        l[hh] *= f;
+                        m[hh] = mn[hh];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float y = __shfl_sync(0xffffffffu, p[j][2 * hh + e], src);
-                                if (j == (key >> 3) && e == (key & 1)) w = y;
-                            }
-                        if (paged_sees(key0 + key, pos[hh], a.window, a.sinks)) {
-#pragma unroll
-                            for (int j = 0; j < 2 * kNd; ++j)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    o[j][2 * hh + e] += w * to_f32<T>(*reinterpret_cast<const T*>(
-                                                                sv + (j >> 3) * kAtom + key * 128 + (((j & 7) ^ (key & 7)) << 4) + (2 * qd + e) * 2));
+                        for (int j = 0; j < 2 * kNd; ++j) {
+                            o[j][2 * hh] *= f;
+                            o[j][2 * hh + 1] *= f;
                         }
                     }
                 }
+                float p[2][4];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const float ms = (m[hh] == -INFINITY ? 0.0f : m[hh]) * a.qscale - kPOff<T>;  // nothing seen yet: all p = 0
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            p[j][2 * hh + e] = ex2(fmaf(sc[j][2 * hh + e], a.qscale, -ms));
+                            l[hh] += p[j][2 * hh + e];
+                        }
+                }
+                // O += P V
+                if (!slow) {
+                    uint32_t pa[4];
+                    pa[0] = pack2_out<T>(p[0][0], p[0][1]);
+                    pa[1] = pack2_out<T>(p[0][2], p[0][3]);
+                    pa[2] = pack2_out<T>(p[1][0], p[1][1]);
+                    pa[3] = pack2_out<T>(p[1][2], p[1][3]);
+#pragma unroll
+                    for (int jj = 0; jj < kNd; ++jj) {
+                        uint32_t b[4];
+                        ldsm4_t(((stage + v_off) ^ ((jj & 3) << 5)) + (jj >> 2) * kAtom, b);
+                        mma16816<T>(o[2 * jj], pa, b[0], b[1]);
+                        mma16816<T>(o[2 * jj + 1], pa, b[2], b[3]);
+                    }
+                } else {
+                    const uint8_t* sv = ring + st * (2 * kHalf) + kHalf + warp * (kStep * 128);
+                    for (int key = 0; key < kStep; ++key) {
+                        const int src = (lane & ~3) | ((key & 7) >> 1);
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            // p of (row, key): tile key / 8, element key % 2, of lane src
+                            float w = 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float y = __shfl_sync(0xffffffffu, p[j][2 * hh + e], src);
+                                    if (j == (key >> 3) && e == (key & 1)) w = y;
+                                }
+                            if (paged_sees(key0 + key, pos[hh], a.window, a.sinks)) {
+#pragma unroll
+                                for (int j = 0; j < 2 * kNd; ++j)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        o[j][2 * hh + e] += w * to_f32<T>(*reinterpret_cast<const T*>(
+                                                                    sv + (j >> 3) * kAtom + key * 128 + (((j & 7) ^ (key & 7)) << 4) + (2 * qd + e) * 2));
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (vb + 1 < vb1 && lane == 0) mbar_arrive(&empty[st]);  // the piece's last stage is the exchange's
             }
-        }
-        loads += nsteps;
-        // Join the four warps' keys: rescale to the common maximum, then add.
+            const bool any = vb1 > vb0;  // else nothing is seen: m = -inf, l = 0, and no stage to exchange in
+            const int last = (blk + kStages - 1) % kStages;
+            float* so = reinterpret_cast<float*>(ring + last * (2 * kHalf));  // [warp][row][D], 8-float groups swizzled by row
+            // Join the four warps' keys: rescale to the common maximum, then add.
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
-            l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
-            if (qd == 0) {
-                s_m[warp][g + 8 * hh] = m[hh];
-                s_l[warp][g + 8 * hh] = l[hh];
+            for (int hh = 0; hh < 2; ++hh) {
+                l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
+                l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
+                if (qd == 0) {
+                    s_m[warp][g + 8 * hh] = m[hh];
+                    s_l[warp][g + 8 * hh] = l[hh];
+                }
             }
-        }
-        __syncthreads();  // also: every warp is done with its ring
-        constexpr int kLdO = D + 8;  // padded rows of the exchange
-        float* so = reinterpret_cast<float*>(ring) + warp * (kRows * kLdO);
+            users_sync();  // also: every warp is done with the last stage
+            if (any) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int row = g + 8 * hh;
-            float mx = s_m[0][row];
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int row = g + 8 * hh;
+                    float mx = s_m[0][row];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][row]);
-            const float f = m[hh] == mx ? 1.0f : ex2((m[hh] - mx) * a.qscale);  // no keys in this warp: 2^-inf = 0
+                    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][row]);
+                    const float f = m[hh] == mx ? 1.0f : ex2((m[hh] - mx) * a.qscale);  // no keys in this warp: 2^-inf = 0
 #pragma unroll
-            for (int j = 0; j < 2 * kNd; ++j)
-                *reinterpret_cast<float2*>(so + row * kLdO + j * 8 + 2 * qd) = make_float2(o[j][2 * hh] * f, o[j][2 * hh + 1] * f);
-        }
-        __syncthreads();
-        const bool whole_tile = x == t.begin && xe == t.begin + t.blocks;
-        const int slot = x == blockIdx.x * line.share ? 0 : 1;
-        if (threadIdx.x == 0 && x == t.begin && !whole_tile)  // this CTA's last piece: the tile goes on in the next ones
-            part_join<D>(a)[blockIdx.x] = Join{static_cast<int>((t.begin + t.blocks - 1) / line.share) - static_cast<int>(blockIdx.x) + 1,
-                                               slot, t.r.start, t.head, t.row0, t.rows};
-        for (int e = threadIdx.x; e < t.rows * (D / 4); e += kThreads) {
-            const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
-            float mx = s_m[0][row], ls = 0.0f;
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][row]);
-            float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                ls += s_m[w][row] == mx ? s_l[w][row] : s_l[w][row] * ex2((s_m[w][row] - mx) * a.qscale);
-                const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring) + (w * kRows + row) * kLdO + d4);
-                v.x += y.x;
-                v.y += y.y;
-                v.z += y.z;
-                v.w += y.w;
+                    for (int j = 0; j < 2 * kNd; ++j)
+                        *reinterpret_cast<float2*>(so + (warp * kRows + row) * D + ((j ^ (row & 3)) * 8) + 2 * qd) =
+                            make_float2(o[j][2 * hh] * f, o[j][2 * hh + 1] * f);
+                }
             }
-            if (whole_tile) {
-                const float inv = mx == -INFINITY ? 0.0f : 1.0f / ls;  // nothing seen: zeros
-                uint2 w2;
-                w2.x = pack2_out<T>(v.x * inv, v.y * inv);
-                w2.y = pack2_out<T>(v.z * inv, v.w * inv);
-                *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row_offset(a, t.r.start, t.head, t.row0 + row, a.ld_out) + d4) = w2;
-            } else {
-                *reinterpret_cast<float4*>(part_o<D>(a, blockIdx.x, slot) + row * D + d4) = v;
-                if (d4 == 0) part_ml<D>(a, blockIdx.x, slot)[row] = make_float2(mx, ls);
+            users_sync();
+            const Tile t = s_piece[buf].t;
+            const int slot = s_piece[buf].slot;
+            for (int e = threadIdx.x; e < t.rows * (D / 4); e += kUsers) {
+                const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
+                float mx = s_m[0][row], ls = 0.0f;
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][row]);
+                float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    ls += s_m[w][row] == mx ? s_l[w][row] : s_l[w][row] * ex2((s_m[w][row] - mx) * a.qscale);
+                    if (!any) continue;
+                    const float4 y = *reinterpret_cast<const float4*>(so + (w * kRows + row) * D + (d4 ^ ((row & 3) << 3)));
+                    v.x += y.x;
+                    v.y += y.y;
+                    v.z += y.z;
+                    v.w += y.w;
+                }
+                if (slot < 0) {
+                    const float inv = mx == -INFINITY ? 0.0f : 1.0f / ls;  // nothing seen: zeros
+                    uint2 w2;
+                    w2.x = pack2_out<T>(v.x * inv, v.y * inv);
+                    w2.y = pack2_out<T>(v.z * inv, v.w * inv);
+                    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row_offset(a, t.r.start, t.head, t.row0 + row, a.ld_out) + d4) = w2;
+                } else {
+                    *reinterpret_cast<float4*>(part_o<D>(a, blockIdx.x, slot) + row * D + d4) = v;
+                    if (d4 == 0) part_ml<D>(a, blockIdx.x, slot)[row] = make_float2(mx, ls);
+                }
             }
+            fence_async_shared();  // the exchange, before the copies that overwrite it
+            users_sync();          // s_m, s_l, the piece and its queries are free, too
+            if (any && lane == 0) mbar_arrive(&empty[last]);
+            if (threadIdx.x == 0) mbar_arrive(&piece_empty[buf]);
         }
-        fence_async_shared();  // the exchange, before the copies that overwrite it
-        __syncthreads();       // the ring is free for the next tile
-        x = xe;
     }
     if (s_abort) {  // a wait ran out: give this CTA's copies in flight time to land
         const unsigned long long t0 = global_timer_ns();
@@ -542,94 +623,100 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
 }
 
 // Joins the pieces of the tile in CTA c's record, c = blockIdx.x:
-// out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M).  A tile may have as many
-// pieces as there are CTAs, so the threads that a tile's rows leave over share
-// the pieces.
+// out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M), kJoinPieces at a time.  A
+// tile may have as many pieces as there are CTAs, so the threads that a tile's
+// rows leave over share the pieces.  A CTA is small enough (registers, shared
+// memory) to be resident beside two of the kernel before it, and waits there.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinPieces = 32;
+constexpr int kJoinSplit = 4;  // CTAs per record, each for a quarter of the dims
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedAttnArgs a) {
-    extern __shared__ float wgt[];  // [pieces][kRows]
-    __shared__ float s_inv[kRows];
+__global__ void __launch_bounds__(kJoinThreads, 6) k_paged_join(const __grid_constant__ PagedAttnArgs a) {
+    constexpr int kQuads = D / 4 / kJoinSplit;  // groups of four dims per row
+    static_assert(kRows * kQuads <= kJoinThreads, "four dims of a row per thread");
+    __shared__ float2 s_ml[kJoinPieces][kRows];  // maximum and sum, then the weight
+    __shared__ float s_m[kRows], s_l[kRows], s_f[kRows];
     __shared__ float4 s_sum[kJoinThreads];
     pdl_wait();
     pdl_trigger();
     const Join t = part_join<D>(a)[blockIdx.x];
     if (t.pieces == 0) return;
     const int64_t c0 = blockIdx.x;
-    const int np = t.pieces;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto slot_of = [&](int i) { return i == 0 ? t.slot : 0; };
-    for (int row = warp; row < t.rows; row += kJoinThreads / 32) {
-        float mx = -INFINITY, ls = 0.0f;
-        for (int i = lane; i < np; i += 32) mx = fmaxf(mx, part_ml<D>(a, c0 + i, slot_of(i))[row].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        for (int i = lane; i < np; i += 32) {
-            const float2 ml = part_ml<D>(a, c0 + i, slot_of(i))[row];
-            const float f = ml.x == mx ? 1.0f : ex2((ml.x - mx) * a.qscale);
-            wgt[i * kRows + row] = f;
-            ls += ml.y * f;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-        if (lane == 0) s_inv[row] = mx == -INFINITY ? 0.0f : 1.0f / ls;
+    const int items = t.rows * kQuads, groups = kJoinThreads / items;
+    const int e = static_cast<int>(threadIdx.x) % items, grp = static_cast<int>(threadIdx.x) / items;
+    const int row = e / kQuads, d4 = (static_cast<int>(blockIdx.y) * kQuads + e % kQuads) * 4;
+    float4 v = make_float4(0, 0, 0, 0);
+    if (threadIdx.x < kRows) {
+        s_m[threadIdx.x] = -INFINITY;
+        s_l[threadIdx.x] = 0.0f;
     }
-    __syncthreads();
-    // four dims of a row per thread; `groups` threads share its pieces
-    const int items = t.rows * (D / 4);
-    const int groups = max(1, kJoinThreads / items);
-    for (int e0 = 0; e0 < items; e0 += kJoinThreads) {
-        const int e = groups > 1 ? static_cast<int>(threadIdx.x) % items : e0 + static_cast<int>(threadIdx.x);
-        const int g = groups > 1 ? static_cast<int>(threadIdx.x) / items : 0;
-        const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
-        float4 v = make_float4(0, 0, 0, 0);
-        if (g < groups && e < items) {
-#pragma unroll 8
-            for (int i = g; i < np; i += groups) {
-                const float f = wgt[i * kRows + row];
-                const float4 y = *reinterpret_cast<const float4*>(part_o<D>(a, c0 + i, slot_of(i)) + row * D + d4);
-                v.x = fmaf(y.x, f, v.x);
-                v.y = fmaf(y.y, f, v.y);
-                v.z = fmaf(y.z, f, v.z);
-                v.w = fmaf(y.w, f, v.w);
+    for (int p0 = 0; p0 < t.pieces; p0 += kJoinPieces) {
+        const int np = min(kJoinPieces, t.pieces - p0);
+        auto slot_of = [&](int i) { return p0 + i == 0 ? t.slot : 0; };
+        __syncthreads();
+        for (int x = threadIdx.x; x < np * kRows; x += kJoinThreads)
+            if (x % kRows < t.rows) s_ml[x / kRows][x % kRows] = part_ml<D>(a, c0 + p0 + x / kRows, slot_of(x / kRows))[x % kRows];
+        __syncthreads();
+        for (int r = warp; r < t.rows; r += kJoinThreads / 32) {
+            const float2 ml = lane < np ? s_ml[lane][r] : make_float2(-INFINITY, 0.0f);
+            float mx = fmaxf(ml.x, s_m[r]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float w = ml.x == mx ? 1.0f : ex2((ml.x - mx) * a.qscale);
+            float l = ml.y * w;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane < np) s_ml[lane][r].x = w;
+            if (lane == 0) {
+                const float f = s_m[r] == mx ? 1.0f : ex2((s_m[r] - mx) * a.qscale);
+                s_f[r] = f;
+                s_l[r] = s_l[r] * f + l;
+                s_m[r] = mx;
             }
         }
-        if (groups > 1) {
-            s_sum[threadIdx.x] = v;
-            __syncthreads();
-            if (g == 0)
-                for (int i = 1; i < groups; ++i) {
-                    const float4 y = s_sum[i * items + e];
-                    v.x += y.x;
-                    v.y += y.y;
-                    v.z += y.z;
-                    v.w += y.w;
-                }
-        }
-        if (g == 0 && e < items) {
-            const float inv = s_inv[row];
-            uint2 w2;
-            w2.x = pack2_out<T>(v.x * inv, v.y * inv);
-            w2.y = pack2_out<T>(v.z * inv, v.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row_offset(a, t.start, t.head, t.row0 + row, a.ld_out) + d4) = w2;
+        __syncthreads();
+        if (grp < groups) {
+            const float f = s_f[row];
+            v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll 4
+            for (int i = grp; i < np; i += groups) {
+                const float w = s_ml[i][row].x;
+                const float4 y = *reinterpret_cast<const float4*>(part_o<D>(a, c0 + p0 + i, slot_of(i)) + row * D + d4);
+                v.x = fmaf(y.x, w, v.x);
+                v.y = fmaf(y.y, w, v.y);
+                v.z = fmaf(y.z, w, v.z);
+                v.w = fmaf(y.w, w, v.w);
+            }
         }
     }
+    s_sum[threadIdx.x] = v;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int i = 1; i < groups; ++i) {
+        const float4 y = s_sum[i * items + e];
+        v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+    }
+    const float inv = s_m[row] == -INFINITY ? 0.0f : 1.0f / s_l[row];
+    uint2 w2;
+    w2.x = pack2_out<T>(v.x * inv, v.y * inv);
+    w2.y = pack2_out<T>(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row_offset(a, t.start, t.head, t.row0 + row, a.ld_out) + d4) = w2;
 }
 
 template <typename T, int D>
 cudaError_t launch_t(PagedAttnArgs a, int num_sms, cudaStream_t st) {
     a.grid = kCtasPerSm * num_sms;
     CUtensorMap tmK, tmV;
-    if (!paged_cache_maps(a.c, kStep, &tmK, &tmV, &a.d_tok, &a.d_head)) return cudaErrorInvalidValue;
-    const int ring = 1024 + kWarps * kStages * 2 * kStep * D * 2;
+    if (!paged_cache_maps(a.c, std::min(a.c.page_size, kBlock), &tmK, &tmV, &a.d_tok, &a.d_head)) return cudaErrorInvalidValue;
+    const int ring = 1024 + kRing<D> * 2 * kBlock * D * 2;
     const int pre = (a.B + 1) * 8;
     auto kern = k_paged_attn<T, D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + pre);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(a.grid), dim3(kThreads), ring + pre, st, tmK, tmV, a);
     if (e != cudaSuccess) return e;
-    const int wgt = a.grid * kRows * 4;
-    return launch_pdl(k_paged_join<T, D>, dim3(a.grid), dim3(kJoinThreads), wgt, st, a);
+    return launch_pdl(k_paged_join<T, D>, dim3(a.grid, kJoinSplit), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace
