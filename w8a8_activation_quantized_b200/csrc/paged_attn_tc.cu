@@ -7,8 +7,8 @@
 // A unit of work is up to 256 rows -- two tiles of 128 / G tokens with their G
 // query heads of one KV head -- against a run of 128-key blocks.  One CTA per
 // SM works through its units:
-//  * warp 0 copies (TMA, 128-byte swizzle) the unit's queries and, block by
-//    block, K and V through a ring of kStages 128-key tiles.  A tile is
+//  * warps 0 and 3 copy (TMA, 128-byte swizzle) the unit's queries and, block by
+//    block, K and V through rings of 128-key tiles.  A tile is
 //    gathered from its pages, one box of 64 dims x page_size keys per page and
 //    half, the page numbers read one block ahead.  Pages that no query of the
 //    unit sees are not read: their boxes lie outside the tensor map, which
@@ -24,12 +24,12 @@
 //    sum are rescaled) only when a row's maximum has grown by a factor of 2^8
 //    or more, which after the first blocks hardly happens.  Weights then reach
 //    2^8 times 2^kOff at most, and the fp32 sums lose nothing by it.
-//  * Rows of V that no query of the unit sees (behind the request's end, or in
-//    front of the window) are zeroed in shared memory before the product that
-//    would multiply them by zero weights: what an unused slot holds may be NaN.
-//    If a row of V that some query of the unit must not see, while others do,
-//    holds NaN or an infinity, the tile's rows are computed again one by one
-//    (redo_row), so that it reaches only the queries that see it.
+//  * Slots behind the request's end, which may hold anything, become zeros in
+//    shared memory before the product that would multiply V there by zero
+//    weights.  Other rows of V are tokens' values: finite, as a rule.  If one that
+//    some query does not see is not, 0 x V makes that query's output NaN; a row
+//    whose output is not finite although its weights' sum is gets computed again
+//    key by key (redo_row), from the keys that it sees alone.
 //
 // What bounds it: per 128 x 128 block of scores the two products take 1024
 // cycles of the tensor pipe at D = 128 (8192 fp16 operations per cycle and SM),
@@ -55,7 +55,7 @@ namespace cider {
 namespace {
 
 constexpr int kKeys = 128;                     // keys per block
-constexpr int kTcThreads = 384;                // warps 0-3: TMA, MMA, two idle; then a softmax warpgroup per tile
+constexpr int kTcThreads = 384;                // warps 0-3: TMA, MMA, idle, TMA; then a softmax warpgroup per tile
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxGrid = 256;                  // CTAs of the tile kernel: one per SM
 constexpr int kMaxCut = 2560;                  // units up to which they may be cut
@@ -66,6 +66,7 @@ constexpr float kLazy = 8.0f;                  // log2 of the growth of a maximu
 // pmin, against blocks [vb0, vb0 + nblk) of its span; slot -1: the whole span.
 struct __align__(16) TcUnit {
     int b, token0, ntok, pmin, vb0, nblk, slot, head;  // head: where the list is cut
+    int len, pad[3];  // the request's keys
 };
 // A unit of several pieces: the first in `slot`, the others in slot 2 c of the
 // CTAs c behind cta.
@@ -88,6 +89,7 @@ struct TcArgs {
     int2* ranges;         // cut: each CTA's first record and their number
     float* part;          // [slot][256][D], then [slot][256] maximum and sum
     int slots;
+    int wide;             // out's rows begin at 32-byte boundaries
     int64_t l2_keys;      // keys whose K and V (all heads) fill 3/5 of the L2
 };
 
@@ -180,6 +182,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
         u.nblk = span_blocks(a, u.pmin, u.ntok);
         u.slot = -1;
         u.head = 0;
+        u.len = keys[u.b];
+        u.pad[0] = u.pad[1] = u.pad[2] = 0;
         return u;
     };
     // this thread's tiles, in order, and the blocks before them
@@ -379,6 +383,14 @@ __device__ __forceinline__ bool group_or(int wg, bool x) {
     return y != 0;
 }
 
+// 32 bytes to a 32-byte boundary: a thread writes whole sectors of its row, where
+// two 16-byte stores would take the warp twice as many passes over its 32 rows.
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 template <int D>
 __device__ __forceinline__ float* part_row(const TcArgs& t, int slot, int row) {
     return t.part + (static_cast<int64_t>(slot) * 256 + row) * D;
@@ -390,7 +402,7 @@ __device__ __forceinline__ float2* part_ml(const TcArgs& t, int slot, int row) {
 
 // One row of a unit on the CUDA cores, key by key: only the keys that this row
 // sees are touched.  Rare (see the top of the file), so it is simple: a first
-// pass over the keys for the maximum and the sum, then one per 32 dims.
+// pass over the keys for the maximum and the sum, then one per 64 dims.
 template <typename T, int D>
 __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const T* q, int pos, T* out,
                                       float* part, float2* ml) {
@@ -401,10 +413,10 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const
     const T* kh = reinterpret_cast<const T*>(a.c.k) + head * a.c.sh;
     const T* vh = reinterpret_cast<const T*>(a.c.v) + head * a.c.sh;
     float m = -INFINITY, l = 0.0f;
-    for (int pass = 0; pass <= D / 32; ++pass) {
-        float o[32];
+    for (int pass = 0; pass <= D / 64; ++pass) {
+        float o[64];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        for (int i = 0; i < 64; ++i) o[i] = 0.0f;
         for (int vb = u.vb0; vb < u.vb0 + u.nblk; ++vb) {
             const int key0 = span.block(vb) * kKeys;
             for (int key = key0; key < key0 + kKeys; ++key) {
@@ -427,9 +439,14 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const
                     m = mn;
                 } else {
                     const float p = ex2(fmaf(s, a.qscale, kOff<T> - m * a.qscale));
-                    const T* v = vh + off + (pass - 1) * 32;
+                    const T* v = vh + off + (pass - 1) * 64;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = fmaf(p, to_f32<T>(v[i]), o[i]);
+                    for (int d = 0; d < 64; d += 8) {
+                        float x[8];
+                        unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(v + d)), x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[d + i] = fmaf(p, x[i], o[d + i]);
+                    }
                 }
             }
         }
@@ -439,29 +456,23 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const
         }
         const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 64; ++i) {
             if (part)
-                part[(pass - 1) * 32 + i] = o[i];
+                part[(pass - 1) * 64 + i] = o[i];
             else
-                out[(pass - 1) * 32 + i] = from_f32<T>(o[i] * inv);
+                out[(pass - 1) * 64 + i] = from_f32<T>(o[i] * inv);
         }
     }
 }
 
-template <typename T>
-__device__ __forceinline__ bool nonfinite8(const uint4& v) {
-    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (w[i] & e) == e || (w[i] & (e << 16)) == (e << 16);
-    return bad;
-}
-
 template <int D>
 constexpr int kTileBytes = kKeys * D * 2;  // one K or V tile; one tile of queries is the same
+// The rings' tiles of keys and of values.  A block's keys are done with when its
+// scores are made, its values a block later.
 template <int D>
-constexpr int kStages = D == 128 ? 5 : 8;
+constexpr int kKStages = D == 128 ? 2 : 4;
+template <int D>
+constexpr int kVStages = D == 128 ? 3 : 4;
 constexpr int kTmemCols = 512;
 
 template <typename T, int D>
@@ -470,14 +481,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                                                             const __grid_constant__ CUtensorMap tmV,
                                                             const __grid_constant__ TcArgs t) {
     constexpr int BF = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
-    constexpr int ST = kStages<D>;
+    constexpr int KS = kKStages<D>, VS = kVStages<D>;
     constexpr int TB = kTileBytes<D>;
     constexpr int AB = kKeys * 128;  // one 64-dim atom of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;               // two tiles of queries
-    uint8_t* sRing = smem + 2 * TB;   // ST tiles of keys or values: K, V, K, V, ...
-    __shared__ uint64_t qfull, qempty, full[ST], empty[ST], sfull[2], pfull[2][2], odone[2];
+    uint8_t* sK = smem + 2 * TB;      // KS tiles of keys
+    uint8_t* sV = sK + KS * TB;       // VS tiles of values
+    __shared__ uint64_t qfull, qempty, kfull[KS], kempty[KS], vfull[VS], vempty[VS], sfull[2], pfull[2][2], odone[2], ufull[2], uempty[2];
+    __shared__ TcUnit s_unit[2];    // the units, one after the other, from the loading warp; nblk < 0: no more
+    __shared__ uint32_t s_lost[8];  // of the last 8 blocks: a bit per box whose page is missing;
     __shared__ uint32_t tmem_slot;
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
@@ -488,15 +502,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
         s_abort = 0;
         mbar_init(&qfull, 1);
         mbar_init(&qempty, 2);
-        for (int s = 0; s < ST; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);  // each tile's products
+        for (int s = 0; s < KS; ++s) {
+            mbar_init(&kfull[s], 1);
+            mbar_init(&kempty[s], 2);  // each tile's products
+        }
+        for (int s = 0; s < VS; ++s) {
+            mbar_init(&vfull[s], 1);
+            mbar_init(&vempty[s], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i][0], 4);  // one arrival per warp
             mbar_init(&pfull[i][1], 4);
             mbar_init(&odone[i], 1);
+            mbar_init(&ufull[i], 1);
+            mbar_init(&uempty[i], 4);  // the values' loader, the issuer and the softmax of each tile
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
@@ -516,38 +536,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
     const int nunits = t.plan->units * a.c.H_kv;
     const int2 range = cut ? t.ranges[blockIdx.x] : make_int2(0, 0);
     const int rounds = cut ? range.y : (nunits + t.grid - 1) / t.grid;
-    // this CTA's unit of round r, and its head; false: it has none
-    auto fetch = [&](int r, TcUnit& u, int& head) {
+    // this CTA's unit of round r; false: it has none
+    auto fetch = [&](int r, TcUnit& u) {
         if (cut) {
             u = t.units[range.x + r];
-            head = u.head;
             return true;
         }
         const int i = static_cast<int>(blockIdx.x);
         const int x = r * t.grid + ((r & 1) ? t.grid - 1 - i : i);
         if (x >= nunits) return false;
         u = t.units[x / a.c.H_kv];
-        head = x % a.c.H_kv;
+        u.head = x % a.c.H_kv;
         return true;
     };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        if (warp == 0) {
-            // ------------------------------ TMA producer ------------------------------
-            int tile = 0, nq = 0;  // tiles of the ring, and queries, so far
+        if (warp == 0 || warp == 3) {
+            // ------------------------------ TMA producers -----------------------------
+            // Warp 0 loads queries and keys, warp 3 values: a lane's copy takes some
+            // 100 cycles to issue, and a block of 16-key pages has 32 of them.
+            const bool keys = warp == 0;
+            int blk = 0, nq = 0;  // blocks and units with queries so far
             bool ok = true;
-            for (int r = 0; r < rounds && ok; ++r) {
-                TcUnit u;
-                int head;
-                if (!fetch(r, u, head) || u.nblk == 0) continue;
+            for (int n = 0, r = 0; ok; ++n) {
+                TcUnit u{};
+                if (keys) {  // posts the units to the other warps
+                    while (r < rounds && !fetch(r, u)) ++r;
+                    if (r++ >= rounds) u.nblk = -1;
+                    ok = mbar_wait(&uempty[n & 1], ((n >> 1) & 1) ^ 1, status, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (lane == 0) {
+                        s_unit[n & 1] = u;
+                        mbar_arrive(&ufull[n & 1]);
+                    }
+                } else {
+                    ok = mbar_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    u = s_unit[n & 1];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&uempty[n & 1]);
+                }
+                if (u.nblk < 0) break;
                 PagedSpan<kKeys> span;
                 span.set(u.pmin, u.pmin + u.ntok - 1, a.window, a.sinks);
                 const int32_t* table = a.table + u.b * a.ld_table;
                 // page of this lane's box of block vb; num_pages (outside the map:
                 // zeros) where no query sees any of its keys, or the page is bad
+                bool missing = false;
                 auto page_of = [&](int vb) {
                     int page = a.c.num_pages;
+                    missing = false;
                     if (lane < t.boxes && vb < u.vb0 + u.nblk) {
                         const int key0 = span.block(vb) * kKeys + lane * t.box_keys;
                         const bool used = key0 <= span.pmax && (a.window <= 0 || key0 + t.box_keys - 1 > span.pmin - a.window || key0 < a.sinks);
@@ -556,42 +595,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                             if (p >= 0 && p < a.c.num_pages)
                                 page = p;
                             else
-                                atomicOr(status, kStatusIndex);
+                                missing = true;
                         }
                     }
+                    if (missing) atomicOr(status, kStatusIndex);
                     return page;
                 };
+                const CUtensorMap* map = keys ? &tmK : &tmV;
+                // one box per page and 64-dim half, a lane each
+                const int box = lane % t.boxes, half = lane / t.boxes;
                 int next = page_of(u.vb0);
-                for (int i = 0; i < u.nblk && ok; ++i) {
-                    const int page = next;
+                for (int i = 0; i < u.nblk && ok; ++i, ++blk) {
+                    const int page = __shfl_sync(0xffffffffu, next, box);
+                    const uint32_t lost = __ballot_sync(0xffffffffu, missing);
                     next = page_of(u.vb0 + i + 1);
-                    const int in_page = (span.block(u.vb0 + i) * kKeys) & (a.c.page_size - 1);  // pages of 256: 0 or 128
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++tile) {
-                        const int s = tile % ST;
-                        ok = ok && mbar_wait(&empty[s], ((tile / ST) & 1) ^ 1, status, abort_flag);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(&full[s], TB);
-                        __syncwarp();
-                        // one box per page and 64-dim half, a lane each
-                        const int box = lane % t.boxes, half = lane / t.boxes;
-                        const int pg = __shfl_sync(0xffffffffu, page, box);
-                        if (half < D / 64) {
-                            const CUtensorMap* map = kv ? &tmV : &tmK;
-                            int c[4] = {half * 64, pg, pg, pg};
-#pragma unroll
-                            for (int d = 1; d < 4; ++d) {
-                                if (d == a.d_tok) c[d] = in_page;
-                                if (d == a.d_head) c[d] = head;
-                            }
-                            tma_load_4d(sRing + s * TB + half * AB + box * t.box_keys * 128, map, &full[s], c[0], c[1], c[2], c[3]);
-                        }
-                        __syncwarp();
+                    const int st = keys ? blk % KS : blk % VS, ph = (keys ? blk / KS : blk / VS) & 1;
+                    uint64_t* full = keys ? &kfull[st] : &vfull[st];
+                    ok = mbar_wait(keys ? &kempty[st] : &vempty[st], ph ^ 1, status, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (lane == 0) {
+                        if (keys) s_lost[blk & 7] = lost;
+                        mbar_arrive_expect_tx(full, TB);
                     }
-                    if (i == 0 && ok) {  // the queries, once the last unit's products are done with theirs
+                    __syncwarp();
+                    if (half < D / 64) {
+                        int c[4] = {half * 64, page, page, page};
+#pragma unroll
+                        for (int d = 1; d < 4; ++d) {
+                            if (d == a.d_tok) c[d] = (span.block(u.vb0 + i) * kKeys) & (a.c.page_size - 1);  // pages of 256: 0 or 128
+                            if (d == a.d_head) c[d] = u.head;
+                        }
+                        tma_load_4d((keys ? sK : sV) + st * TB + half * AB + box * t.box_keys * 128, map, full, c[0], c[1], c[2], c[3]);
+                    }
+                    __syncwarp();
+                    if (keys && i == 0) {  // the queries, once the last unit's products are done with theirs
                         ok = mbar_wait(&qempty, (nq & 1) ^ 1, status, abort_flag);
                         ok = __all_sync(0xffffffffu, ok);
                         const int tiles = u.ntok > t.tok ? 2 : 1;
@@ -600,7 +637,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                             mbar_arrive_expect_tx(&qfull, tiles * (D / 64) * bytes);
                             for (int h = 0; h < tiles; ++h)
                                 for (int d = 0; d < D / 64; ++d)
-                                    tma_load_3d(sQ + h * TB + d * AB, &tmQ, &qfull, d * 64, head * a.G, u.token0 + h * t.tok);
+                                    tma_load_3d(sQ + h * TB + d * AB, &tmQ, &qfull, d * 64, u.head * a.G, u.token0 + h * t.tok);
                         }
                         __syncwarp();
                         ++nq;
@@ -613,16 +650,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             // registers; one lane issues.
             constexpr uint32_t idesc_s = idesc_16(128, kKeys, BF, 0);
             constexpr uint32_t idesc_o = idesc_16(128, D, BF, 1);
-            const uint32_t q_lo = desc_lo(smem_u32(sQ), 0), k_lo = desc_lo(smem_u32(sRing), 0), v_lo = desc_lo(smem_u32(sRing), AB);
+            const uint32_t q_lo = desc_lo(smem_u32(sQ), 0), k_lo = desc_lo(smem_u32(sK), 0), v_lo = desc_lo(smem_u32(sV), AB);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const bool leader = elect_one();
-            int tile = 0, nq = 0, blk[2] = {0, 0};  // blk: blocks of each tile so far
+            int gb = 0, nq = 0, blk[2] = {0, 0};  // the rings' blocks and units so far, and the blocks of each tile
             bool ok = true;
-            for (int r = 0; r < rounds && ok; ++r) {
-                TcUnit u;
-                int head;
-                if (!fetch(r, u, head)) continue;
-                const int nblk = __shfl_sync(0xffffffffu, u.nblk, 0), tiles = __shfl_sync(0xffffffffu, u.ntok, 0) > t.tok ? 2 : 1;
+            for (int n = 0; ok; ++n) {
+                ok = mbar_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const int nblk = s_unit[n & 1].nblk, tiles = s_unit[n & 1].ntok > t.tok ? 2 : 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&uempty[n & 1]);
+                if (nblk < 0) break;
                 if (nblk == 0) continue;
                 auto scores = [&](int h, int s) {  // S_h = Q_h K^T
                     if (leader) {
@@ -635,21 +674,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                         umma_commit(&sfull[h]);
                     }
                 };
-                {
-                    const int s = tile % ST;
-                    ok = mbar_wait(&full[s], (tile / ST) & 1, status, abort_flag) && mbar_wait(&qfull, nq & 1, status, abort_flag);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    tc_fence_after();
-                    for (int h = 0; h < tiles; ++h) scores(h, s);
-                    ++tile;
-                }
+                ok = mbar_wait(&kfull[gb % KS], (gb / KS) & 1, status, abort_flag) && mbar_wait(&qfull, nq & 1, status, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                for (int h = 0; h < tiles; ++h) scores(h, gb % KS);
                 ++nq;
-                for (int i = 0; i < nblk && ok; ++i) {
-                    const int sv = tile % ST, vph = (tile / ST) & 1;
-                    const int sk = (tile + 1) % ST, kph = ((tile + 1) / ST) & 1;
+                for (int i = 0; i < nblk && ok; ++i, ++gb) {
+                    const int sv = gb % VS, sk = (gb + 1) % KS;
                     const bool more = i + 1 < nblk;
                     for (int h = 0; h < tiles; ++h) {
-                        if (h == 0) ok = mbar_wait(&full[sv], vph, status, abort_flag);
+                        if (h == 0) ok = mbar_wait(&vfull[sv], (gb / VS) & 1, status, abort_flag);
                         const uint32_t v0 = v_lo + sv * (TB >> 4);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -669,7 +703,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                         ++blk[h];
                         if (more) {
                             if (h == 0) {
-                                ok = mbar_wait(&full[sk], kph, status, abort_flag);
+                                ok = mbar_wait(&kfull[sk], ((gb + 1) / KS) & 1, status, abort_flag);
                                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                                 tc_fence_after();
                             }
@@ -677,7 +711,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                         }
                     }
                     if (!ok) break;
-                    tile += more ? 2 : 1;
                 }
             }
         }
@@ -690,15 +723,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_addr + h * 128, tO = tmem + lane_addr + 256 + h * D;
         int nb = 0, nu = 0;  // blocks and units of this tile so far
-        int vtile = 0; // the ring's index of the unit's first K tile
+        int gb = 0;    // the rings' blocks before this unit
         bool ok = true;
-        for (int r = 0; r < rounds && ok; ++r) {
-            TcUnit u;
-            int head;
-            if (!fetch(r, u, head)) continue;
+        for (int n = 0;; ++n) {
+            if (ok) ok = mbar_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
+            const TcUnit u = s_unit[n & 1];
+            if (group_or(h, !ok || u.nblk < 0)) break;  // the group's warps go on, or end, together (and have read it)
+            if (row == 0) mbar_arrive(&uempty[n & 1]);
+            const int head = u.head;
             const int tok0 = h * t.tok, ntok = min(t.tok, u.ntok - tok0);  // this tile's tokens
             if (ntok <= 0) {
-                vtile += 2 * u.nblk;
+                gb += u.nblk;
                 continue;
             }
             PagedSpan<kKeys> span;
@@ -707,19 +742,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             const int tok = row / a.G;
             const int pos = pmin + tok;
             const bool live = tok < ntok && row < t.tok * a.G;
-            const int32_t* table = a.table + u.b * a.ld_table;
-            // does any block that some query of the unit sees lack its page?
-            bool bad = false;
-            for (int e = row; e < u.nblk * t.boxes; e += 128) {
-                const int key0 = span.block(u.vb0 + e / t.boxes) * kKeys + (e % t.boxes) * t.box_keys;
-                if (key0 <= span.pmax && (a.window <= 0 || key0 + t.box_keys - 1 > span.pmin - a.window || key0 < a.sinks)) {
-                    const int p = __ldg(table + (key0 >> a.c.ps_log2));
-                    bad |= p < 0 || p >= a.c.num_pages;
-                }
-            }
-            bad = group_or(h, bad);
             float m = -INFINITY, l = 0.0f;
-            bool poison = false;
             // One thread tells the producer what this tile's products are done with
             // (and for the second tile, where the unit has none).
             const int frees = row != 0 ? 0 : u.ntok > t.tok ? 1 : 2;
@@ -732,79 +755,69 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 }
                 tc_fence_after();
                 for (int e = 0; e < frees; ++e) {  // QK^T of this block and PV of the last one are done
-                    mbar_arrive(&empty[(vtile + 2 * i) % ST]);
-                    if (i > 0) mbar_arrive(&empty[(vtile + 2 * i - 1) % ST]);
+                    mbar_arrive(&kempty[(gb + i) % KS]);
+                    if (i > 0) mbar_arrive(&vempty[(gb + i - 1) % VS]);
                     if (i + 1 == u.nblk) mbar_arrive(&qempty);
                 }
                 float low = -FLT_MAX;  // a row that has seen a key has a finite maximum
-                const bool whole = !bad && key0 + kKeys - 1 <= pmin &&
+                const uint32_t lost = s_lost[(gb + i) & 7];
+                const bool whole = !lost && key0 + kKeys - 1 <= pmin &&
                                    (a.window <= 0 || key0 > pmax - a.window || key0 + kKeys <= a.sinks);
                 if (!whole) {
-                    // V: zero the rows that no query of the unit sees; look for
-                    // NaN and infinities in the others
-                    const int vt = vtile + 2 * i + 1, s = vt % ST;
-                    ok = mbar_wait(&full[s], (vt / ST) & 1, status, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
+                    if (key0 + kKeys > u.len) {  // slots behind the request's end: V becomes zeros there
+                        const int s = (gb + i) % VS;
+                        ok = mbar_wait(&vfull[s], ((gb + i) / VS) & 1, status, abort_flag);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        for (int e = row; e < kKeys * (D / 8); e += 128)
+                            if (key0 + ((e >> 3) & (kKeys - 1)) >= u.len) reinterpret_cast<uint4*>(sV + s * TB)[e] = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
                     }
-#pragma unroll 2
-                    for (int e = row; e < kKeys * (D / 8); e += 128) {
-                        const int key = key0 + ((e >> 3) & (kKeys - 1));
-                        uint4* v = reinterpret_cast<uint4*>(sRing + s * TB) + e;
-                        const bool used = key <= span.pmax && (a.window <= 0 || key > span.pmin - a.window || key < a.sinks);
-                        if (!used)
-                            *v = make_uint4(0, 0, 0, 0);
-                        else
-                            poison |= nonfinite8<T>(*v);
-                    }
-                    fence_async_smem();
-                    // S: -inf where the row does not see the key, 32 columns at a
+                    // S: -inf where the row does not see the key, 64 columns at a
                     // time and back to tensor memory, so that the registers hold
                     // the 128 scores only once (a spill goes to L2: shared memory
                     // leaves no L1)
-                    uint32_t pages = 0xff;  // bit per box: has a page
-                    if (bad) {
-                        pages = 0;
-                        for (int e = 0; e < t.boxes; ++e) {
-                            const int k0 = key0 + e * t.box_keys;
-                            if (k0 <= span.pmax && (a.window <= 0 || k0 + t.box_keys - 1 > span.pmin - a.window || k0 < a.sinks)) {
-                                const int p = __ldg(table + (k0 >> a.c.ps_log2));
-                                if (p >= 0 && p < a.c.num_pages) pages |= 1u << e;
-                            }
-                        }
-                    }
                     const int last = pos - key0;                                             // seen: x <= last
                     const int first = a.window > 0 ? max(pos - a.window, -1) - key0 : -1;    // and x > first
                     const int sink = a.window > 0 ? max(min(a.sinks - key0, kKeys), 0) : 0;  // or x < sink
-                    const int box_log2 = 31 - __clz(t.box_keys);
-                    bool any = false;
+                    uint32_t any = 0;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32];
-                        tmem_ld_32x32b_x32(tS + c * 32, x);
-                        // the row's seen columns of this chunk as bits
-                        const int lo = c * 32;
-                        const uint32_t below = last - lo >= 31 ? ~0u : last < lo ? 0u : (2u << (last - lo)) - 1;
-                        const uint32_t after = first < lo ? ~0u : first - lo >= 31 ? 0u : ~((2u << (first - lo)) - 1);
-                        const uint32_t sinks = sink <= lo ? 0u : sink - lo >= 32 ? ~0u : (1u << (sink - lo)) - 1;
-                        uint32_t see = below & (after | sinks);
-                        if (bad)
-                            for (int e = 0; e < 32; e += 16)  // pages hold 16 keys or more
-                                if (!((pages >> ((lo + e) >> box_log2)) & 1u)) see &= ~(0xffffu << e);
-                        any |= see != 0;
-                        ld_wait(x);
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t x[2][32];
+                        tmem_ld_32x32b_x32(tS + half * 64, x[0]);
+                        tmem_ld_32x32b_x32(tS + half * 64 + 32, x[1]);
+                        uint32_t see[2];  // the row's seen columns as bits
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((see >> e) & 1u)) x[e] = 0xff800000u;  // -inf
-                        tmem_st_32x32b_x32(tS + c * 32, x);
+                        for (int c = 0; c < 2; ++c) {
+                            const int lo = half * 64 + c * 32;
+                            const uint32_t below = last - lo >= 31 ? ~0u : last < lo ? 0u : (2u << (last - lo)) - 1;
+                            const uint32_t after = first < lo ? ~0u : first - lo >= 31 ? 0u : ~((2u << (first - lo)) - 1);
+                            const uint32_t sinks = sink <= lo ? 0u : sink - lo >= 32 ? ~0u : (1u << (sink - lo)) - 1;
+                            see[c] = below & (after | sinks);
+                            if (lost)
+                                for (int e = 0; e < 32; e += 16)  // pages hold 16 keys or more
+                                    if ((lost >> ((lo + e) / t.box_keys)) & 1u) see[c] &= ~(0xffffu << e);
+                            any |= see[c];
+                        }
+                        ld_wait(x[0]);
+                        ld_wait(x[1]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((see[c] >> e) & 1u)) x[c][e] = 0xff800000u;  // -inf
+                            tmem_st_32x32b_x32(tS + half * 64 + c * 32, x[c]);
+                        }
                     }
                     tmem_st_wait();
                     if (!any) low = -INFINITY;
                 }
                 // Maximum of the row (the reference moves only if it grew by 2^kLazy),
                 // in four chains; the upper 64 columns first, which are read again
-                // for their weights.
+                // for their weights (all 128 would be spilled in places, and a spill
+                // goes to L2: shared memory leaves no L1).
                 uint32_t sr[2][32];
                 float mc[4];
 #pragma unroll
@@ -874,30 +887,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 const uint64_t ls = add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3]));
                 l += lo_f32(ls) + hi_f32(ls);
             }
-            vtile += 2 * u.nblk;
+            gb += u.nblk;
             if (u.nblk > 0 && ok) {
                 ok = mbar_wait(&odone[h], nu & 1, status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
-                for (int e = 0; e < frees; ++e) mbar_arrive(&empty[(vtile - 1) % ST]);
+                for (int e = 0; e < frees; ++e) mbar_arrive(&vempty[(gb - 1) % VS]);
                 ++nu;
             }
-            poison = group_or(h, poison);
-            ok = !group_or(h, !ok);  // the group's warps go on, or end, together
-            if (!ok) break;
+            if (!ok) continue;  // ends above, with the group's other warps
             const int slot = u.slot;
             const int64_t q_row = u.token0 + tok0 + tok;
             const int64_t q_col = static_cast<int64_t>(head * a.G + (row - tok * a.G)) * D;
             T* out = static_cast<T*>(a.out) + q_row * a.ld_out + q_col;
-            if (poison) {
-                if (live)
-                    redo_row<T, D>(t, u, head, static_cast<const T*>(a.q) + q_row * a.ld_q + q_col, pos, out,
-                                   slot >= 0 ? part_row<D>(t, slot, h * 128 + row) : nullptr,
-                                   slot >= 0 ? part_ml<D>(t, slot, h * 128 + row) : nullptr);
-                continue;
-            }
             const float inv = m == -INFINITY ? 0.0f : 1.0f / l;  // nothing seen: zeros
             if (slot >= 0 && live) *part_ml<D>(t, slot, h * 128 + row) = make_float2(m, l);
+            bool odd = false;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -909,23 +914,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     for (int e = 0; e < 32; ++e) o[e] = 0;
                 }
                 if (!live) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) odd |= (o[e] & 0x7f800000u) == 0x7f800000u;
                 if (slot >= 0) {
-                    float4* p = reinterpret_cast<float4*>(part_row<D>(t, slot, h * 128 + row) + c * 32);
+                    float* p = part_row<D>(t, slot, h * 128 + row) + c * 32;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        p[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
-                                           __uint_as_float(o[4 * e + 3]));
+                    for (int e = 0; e < 4; ++e) store32(p + 8 * e, o + 8 * e);
                 } else {
-                    uint4* p = reinterpret_cast<uint4*>(out + c * 32);
+                    uint32_t y[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v[8];
+                    for (int e = 0; e < 16; ++e)
+                        y[e] = m == -INFINITY ? 0u : pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    if (t.wide) {
+                        store32(out + c * 32, y);
+                        store32(out + c * 32 + 16, y + 8);
+                    } else {
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) v[x] = m == -INFINITY ? 0.0f : __uint_as_float(o[8 * e + x]) * inv;
-                        p[e] = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4*>(out + c * 32)[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                     }
                 }
             }
+            // NaN or an infinity in O although the weights' sum is finite: it came from V,
+            // perhaps from a row of it that this query does not see.
+            if (odd && live && l < INFINITY)
+                redo_row<T, D>(t, u, head, static_cast<const T*>(a.q) + q_row * a.ld_q + q_col, pos, out,
+                               slot >= 0 ? part_row<D>(t, slot, h * 128 + row) : nullptr,
+                               slot >= 0 ? part_ml<D>(t, slot, h * 128 + row) : nullptr);
             tc_fence_before();
         }
     }
@@ -1030,6 +1045,7 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
     t.boxes = kKeys / t.box_keys;
     t.grid = std::min(num_sms, kMaxGrid);
     t.slots = 2 * t.grid;
+    t.wide = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ld_out) * 2) & 31) == 0;
     int dev = 0, l2 = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || (e = cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev)) != cudaSuccess) return e;
@@ -1052,7 +1068,7 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
     if (!encode_tensor_map(&tmQ, type, 3, const_cast<void*>(p.q), qd, qs, qb, ones, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
 
-    const int smem = 1024 + (2 + kStages<D>) * kTileBytes<D>;
+    const int smem = 1024 + (2 + kKStages<D> + kVStages<D>) * kTileBytes<D>;
     auto kern = k_paged_tc<T, D>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     const int plan_smem = (4 * p.B + 1) * 4;
