@@ -18,8 +18,8 @@
 //    softmax runs while the tensor pipe works for the other tile.
 //  * two warpgroups do the softmax, one per tile, one thread per row (no
 //    shuffles): S_t from tensor memory, mask, maximum, weights, sum; P_t goes
-//    back in 16 bits over S_t's first 64 columns and is the product's operand
-//    from there.  O_t stays in tensor memory (S 2 x 128, O 2 x D columns).
+//    back in 16 bits, over S_t's first 64 columns or (D = 64) beside, and is the
+//    product's operand from there.  O_t stays in tensor memory.
 //    The maximum is a reference, not the exact one: it moves (and O_t and the
 //    sum are rescaled) only when a row's maximum has grown by a factor of 2^8
 //    or more, which after the first blocks hardly happens.  Weights then reach
@@ -56,7 +56,7 @@ namespace {
 
 constexpr int kKeys = 128;                     // keys per block
 constexpr int kTcThreads = 384;                // warps 0-3: TMA, MMA, idle, TMA; then a softmax warpgroup per tile
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;  // fewer threads, cheaper barriers: a prompt of 2048 52.8 us with 1024, 48.9 with 256
 constexpr int kMaxGrid = 256;                  // CTAs of the tile kernel: one per SM
 constexpr int kMaxCut = 2560;                  // units up to which they may be cut
 constexpr int kMinShare = 2;                   // blocks per CTA where they are cut
@@ -474,6 +474,12 @@ constexpr int kKStages = D == 128 ? 2 : 4;
 template <int D>
 constexpr int kVStages = D == 128 ? 3 : 4;
 constexpr int kTmemCols = 512;
+// Whether P has columns of its own (S 2 x 128, O 2 x D, P 2 x 64).  Then the next
+// block's scores are made as soon as the last one's have been read, and a tile's
+// softmax waits for no product; where P lies over S, they wait for the product
+// that reads it.
+template <int D>
+constexpr bool kApart = D == 64;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constant__ CUtensorMap tmQ,
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
     uint8_t* sQ = smem;               // two tiles of queries
     uint8_t* sK = smem + 2 * TB;      // KS tiles of keys
     uint8_t* sV = sK + KS * TB;       // VS tiles of values
-    __shared__ uint64_t qfull, qempty, kfull[KS], kempty[KS], vfull[VS], vempty[VS], sfull[2], pfull[2][2], odone[2], ufull[2], uempty[2];
+    __shared__ uint64_t qfull, qempty, kfull[KS], kempty[KS], vfull[VS], vempty[VS], sfull[2], pfull[2][2], sfree[2], odone[2][2], turn[4][2], ufull[2], uempty[2];
     __shared__ TcUnit s_unit[2];    // the units, one after the other, from the loading warp; nblk < 0: no more
     __shared__ uint32_t s_lost[8];  // of the last 8 blocks: a bit per box whose page is missing;
     __shared__ uint32_t tmem_slot;
@@ -508,13 +514,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
         }
         for (int s = 0; s < VS; ++s) {
             mbar_init(&vfull[s], 1);
-            mbar_init(&vempty[s], 2);
+            mbar_init(&vempty[s], kApart<D> ? 1 : 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i][0], 4);  // one arrival per warp
             mbar_init(&pfull[i][1], 4);
-            mbar_init(&odone[i], 1);
+            mbar_init(&sfree[i], 4);
+            for (int w = 0; w < 4; ++w) mbar_init(&turn[w][i], 1);
+            mbar_init(&odone[i][0], 1);
+            mbar_init(&odone[i][1], 1);
             mbar_init(&ufull[i], 1);
             mbar_init(&uempty[i], 4);  // the values' loader, the issuer and the softmax of each tile
         }
@@ -677,31 +686,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 ok = mbar_wait(&kfull[gb % KS], (gb / KS) & 1, status, abort_flag) && mbar_wait(&qfull, nq & 1, status, abort_flag);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
-                for (int h = 0; h < tiles; ++h) scores(h, gb % KS);
+                // O_h (+)= P_h V of 64 keys, V in stage sv
+                auto values = [&](int h, int half, int sv, bool first) {
+                    if (leader) {
+                        const uint32_t v0 = v_lo + sv * (TB >> 4), p0 = kApart<D> ? 384 + h * 64 : h * 128;
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4) {  // 16 keys: 8 columns of P, 2 KB of each atom of V
+                            const int kk = half * 4 + k4;
+                            mma_ts(tm + 256 + h * D, tm + p0 + kk * 8, v0 + (kk * 2048 >> 4), idesc_o, !first || k4 > 0);
+                        }
+                    }
+                };
+                for (int h = 0; h < tiles && ok; ++h) {
+                    if (kApart<D> && blk[h] > 0) {
+                        ok = mbar_wait(&sfree[h], (blk[h] - 1) & 1, status, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        tc_fence_after();
+                    }
+                    if (ok) scores(h, gb % KS);
+                }
                 ++nq;
                 for (int i = 0; i < nblk && ok; ++i, ++gb) {
                     const int sv = gb % VS, sk = (gb + 1) % KS;
                     const bool more = i + 1 < nblk;
+                    if (kApart<D> && more) {  // the next scores first: they need only the last ones read
+                        ok = mbar_wait(&kfull[sk], ((gb + 1) / KS) & 1, status, abort_flag);
+                        for (int h = 0; h < tiles; ++h) {
+                            ok = ok && mbar_wait(&sfree[h], blk[h] & 1, status, abort_flag);
+                            ok = __all_sync(0xffffffffu, ok);
+                            tc_fence_after();
+                            if (ok) scores(h, sk);
+                        }
+                    }
                     for (int h = 0; h < tiles; ++h) {
-                        if (h == 0) ok = mbar_wait(&vfull[sv], (gb / VS) & 1, status, abort_flag);
-                        const uint32_t v0 = v_lo + sv * (TB >> 4);
+                        if (h == 0) ok = ok && mbar_wait(&vfull[sv], (gb / VS) & 1, status, abort_flag);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             ok = ok && mbar_wait(&pfull[h][half], blk[h] & 1, status, abort_flag);
                             ok = __all_sync(0xffffffffu, ok);
                             tc_fence_after();
-                            if (ok && leader) {
-#pragma unroll
-                                for (int k4 = 0; k4 < 4; ++k4) {  // 16 keys: 8 columns of P, 2 KB of each atom of V
-                                    const int kk = half * 4 + k4;
-                                    mma_ts(tm + 256 + h * D, tm + h * 128 + kk * 8, v0 + (kk * 2048 >> 4), idesc_o, i > 0 || kk > 0);
-                                }
-                            }
+                            if (ok) values(h, half, sv, i == 0 && half == 0);
                         }
                         if (!ok) break;
-                        if (!more && leader) umma_commit(&odone[h]);
+                        if (leader && (kApart<D> || !more)) umma_commit(&odone[h][kApart<D> ? blk[h] & 1 : 0]);
                         ++blk[h];
-                        if (more) {
+                        if (!kApart<D> && more) {
                             if (h == 0) {
                                 ok = mbar_wait(&kfull[sk], ((gb + 1) / KS) & 1, status, abort_flag);
                                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -710,7 +739,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                             scores(h, sk);
                         }
                     }
-                    if (!ok) break;
+                    if (ok && kApart<D> && leader) umma_commit(&vempty[sv]);
                 }
             }
         }
@@ -722,7 +751,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_addr + h * 128, tO = tmem + lane_addr + 256 + h * D;
+        const uint32_t tP = kApart<D> ? tmem + lane_addr + 384 + h * 64 : tS;
         int nb = 0, nu = 0;  // blocks and units of this tile so far
+        uint32_t turns = 0;  // of this warp at the exponentials
         int gb = 0;    // the rings' blocks before this unit
         bool ok = true;
         for (int n = 0;; ++n) {
@@ -746,6 +777,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             // One thread tells the producer what this tile's products are done with
             // (and for the second tile, where the unit has none).
             const int frees = row != 0 ? 0 : u.ntok > t.tok ? 1 : 2;
+            // Where no product keeps the tiles apart in time, the two warps that share a
+            // scheduler take turns at the exponentials: at the same time each would take
+            // twice as long, and then leave the special-function unit idle together.
+            const bool paired = kApart<D> && u.ntok > t.tok && u.nblk > 0;
+            uint64_t* my_turn = &turn[warp & 3][h];
+            uint64_t* other_turn = &turn[warp & 3][h ^ 1];
+            if (paired && h == 1 && lane == 0) mbar_arrive(other_turn);
             for (int i = 0; i < u.nblk; ++i, ++nb) {
                 const int key0 = span.block(u.vb0 + i) * kKeys;
                 ok = mbar_wait(&sfull[h], nb & 1, status, abort_flag);
@@ -756,7 +794,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 tc_fence_after();
                 for (int e = 0; e < frees; ++e) {  // QK^T of this block and PV of the last one are done
                     mbar_arrive(&kempty[(gb + i) % KS]);
-                    if (i > 0) mbar_arrive(&vempty[(gb + i - 1) % VS]);
+                    if (!kApart<D> && i > 0) mbar_arrive(&vempty[(gb + i - 1) % VS]);
                     if (i + 1 == u.nblk) mbar_arrive(&qempty);
                 }
                 float low = -FLT_MAX;  // a row that has seen a key has a finite maximum
@@ -815,23 +853,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     if (!any) low = -INFINITY;
                 }
                 // Maximum of the row (the reference moves only if it grew by 2^kLazy),
-                // in four chains; the upper 64 columns first, which are read again
-                // for their weights (all 128 would be spilled in places, and a spill
-                // goes to L2: shared memory leaves no L1).
-                uint32_t sr[2][32];
-                float mc[4];
+                // in four chains.  Where P lies over S, the upper 64 columns come first and
+                // are read again for their weights: that leaves registers.
+                uint32_t sr[kApart<D> ? 4 : 2][32];
+                float mc[4] = {low, low, low, low};
+                auto maxima = [&](const uint32_t (&x)[32], int c) {
 #pragma unroll
-                for (int half = 1; half >= 0; --half) {
+                    for (int e = 0; e < 32; e += 2)
+                        mc[2 * c + (e >> 4)] = max3_nan(mc[2 * c + (e >> 4)], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                };
+                if constexpr (kApart<D>) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(tS + half * 64 + c * 32, sr[c]);
-                    ld_wait(sr[0]);
-                    ld_wait(sr[1]);
+                    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, sr[c]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (half) mc[c] = low;
+                    for (int c = 0; c < 4; ++c) ld_wait(sr[c]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sfree[h]);  // S may be overwritten
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2)
-                            mc[c] = max3_nan(mc[c], __uint_as_float(sr[c >> 1][(c & 1) * 16 + e]), __uint_as_float(sr[c >> 1][(c & 1) * 16 + e + 1]));
+                    for (int c = 0; c < 4; ++c) maxima(sr[c], c & 1);
+                } else {
+#pragma unroll
+                    for (int half = 1; half >= 0; --half) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(tS + half * 64 + c * 32, sr[c]);
+                        ld_wait(sr[0]);
+                        ld_wait(sr[1]);
+                        maxima(sr[0], 0);
+                        maxima(sr[1], 1);
                     }
                 }
                 const float mx = max3_nan(max3_nan(mc[0], mc[1], mc[2]), mc[3], mc[3]);
@@ -843,6 +892,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     f = ex2((m - mx) * a.qscale);
                     m = mx == INFINITY ? NAN : mx;
                     l *= f;
+                }
+                if (kApart<D> && i > 0) {  // the last block's product is done: with P, and O is complete
+                    if (ok) ok = mbar_wait(&odone[h][(nb - 1) & 1], ((nb - 1) >> 1) & 1, status, abort_flag);
+                    __syncwarp();
+                    tc_fence_after();
                 }
                 if (i > 0 && __any_sync(0xffffffffu, grow)) {  // O is complete up to the last block
 #pragma unroll 1
@@ -859,40 +913,64 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 const float ms = kOff<T> - (m == -INFINITY ? 0.0f : m) * a.qscale;  // nothing seen yet: all weights 0
                 const uint64_t qs2 = pack_f32x2(a.qscale, a.qscale), ms2 = pack_f32x2(ms, ms);
                 uint64_t l2[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t p[32];
-                    if (c == 1) {
-                        ld_wait(sr[0]);
-                        ld_wait(sr[1]);
-                    }
+                // 64 keys' weights, from the scores in x[0] and x[1]
+                auto weights = [&](const uint32_t (*x)[32], uint32_t (&p)[32]) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const uint32_t* s2 = &sr[e >> 4][(2 * e) & 31];
-                        const uint64_t x = fma_f32x2((static_cast<uint64_t>(s2[1]) << 32) | s2[0], qs2, ms2);
-                        const uint64_t w = pack_f32x2(ex2(lo_f32(x)), ex2(hi_f32(x)));
+                        const uint32_t* s2 = &x[e >> 4][(2 * e) & 31];
+                        const uint64_t y = fma_f32x2((static_cast<uint64_t>(s2[1]) << 32) | s2[0], qs2, ms2);
+                        const uint64_t w = pack_f32x2(ex2(lo_f32(y)), ex2(hi_f32(y)));
                         l2[e & 3] = add_f32x2(l2[e & 3], w);
                         p[e] = pack2<T>(lo_f32(w), hi_f32(w));
                     }
-                    tmem_st_32x32b_x32(tS + c * 32, p);
-                    if (c == 0) {
-                        tmem_ld_32x32b_x32(tS + 64, sr[0]);
-                        tmem_ld_32x32b_x32(tS + 96, sr[1]);
+                };
+                if constexpr (kApart<D>) {
+                    uint32_t p[2][32];
+                    if (paired) {
+                        if (ok) ok = mbar_wait(my_turn, turns++ & 1, status, abort_flag);
+                        __syncwarp();
                     }
+                    weights(sr, p[0]);
+                    weights(sr + 2, p[1]);
+                    if (paired && lane == 0 && !(h == 1 && i + 1 == u.nblk)) mbar_arrive(other_turn);
+                    tmem_st_32x32b_x32(tP, p[0]);
+                    tmem_st_32x32b_x32(tP + 32, p[1]);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[h][c]);  // 64 keys' weights: their half of the product may start
+                    if (lane == 0) {
+                        mbar_arrive(&pfull[h][0]);
+                        mbar_arrive(&pfull[h][1]);
+                    }
+                } else {
+                    uint32_t p[32];
+                    weights(sr, p);
+                    tmem_st_32x32b_x32(tS, p);
+                    tmem_ld_32x32b_x32(tS + 64, sr[0]);
+                    tmem_ld_32x32b_x32(tS + 96, sr[1]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[h][0]);  // 64 keys' weights: their half of the product may start
+                    ld_wait(sr[0]);
+                    ld_wait(sr[1]);
+                    weights(sr, p);
+                    tmem_st_32x32b_x32(tS + 32, p);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[h][1]);
                 }
                 const uint64_t ls = add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3]));
                 l += lo_f32(ls) + hi_f32(ls);
             }
             gb += u.nblk;
             if (u.nblk > 0 && ok) {
-                ok = mbar_wait(&odone[h], nu & 1, status, abort_flag);
+                ok = kApart<D> ? mbar_wait(&odone[h][(nb - 1) & 1], ((nb - 1) >> 1) & 1, status, abort_flag)
+                               : mbar_wait(&odone[h][0], nu & 1, status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
-                for (int e = 0; e < frees; ++e) mbar_arrive(&vempty[(gb - 1) % VS]);
+                for (int e = 0; !kApart<D> && e < frees; ++e) mbar_arrive(&vempty[(gb - 1) % VS]);
                 ++nu;
             }
             if (!ok) continue;  // ends above, with the group's other warps
