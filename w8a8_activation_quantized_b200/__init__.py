@@ -525,22 +525,22 @@ def cider_paged_tables(cached, fresh, free_pages, block_table, page_size, num_pa
     each request has in the cache and brings; free_pages: int32 pages, taken in
     order; block_table: int32 [B, width], filled behind the pages that each
     request has; rows: rows of the packed batch.
-    -> (cu_fresh [B + 1], kv_len [B], slots [rows], taken [1]), all int32; the
-    ones that are not given share one allocation."""
+    -> (cu_fresh [B + 1], kv_len [B], slots [rows], taken [1]), all int32: the
+    four that are given, or new ones that share one allocation."""
     B = cached.numel()
     ld, width = _table(block_table, B)
     if fresh.numel() != B:
         raise ValueError("cached and fresh are [B]")
-    sizes = (B + 1, B, rows, 1)
-    out = [cu_fresh, kv_len, slots, taken]
-    if any(t is None for t in out):
-        need = [n for n, t in zip(sizes, out) if t is None]
-        parts = iter(_empty(sum(need), torch.int32, block_table.device, stream).split_with_sizes(need))
-        out = [next(parts) if t is None else t for t in out]
-    cu_fresh, kv_len, slots, taken = out
-    if cu_fresh.numel() != B + 1 or kv_len.numel() != B or slots.numel() != rows or taken.numel() != 1:
-        raise ValueError("cu_fresh is [B + 1], kv_len [B], slots [rows] and taken [1]")
-    given = (cached, fresh, free_pages, cu_fresh, kv_len, slots, taken)
+    given = [cached, fresh, free_pages]
+    if cu_fresh is None and kv_len is None and slots is None and taken is None:
+        cu_fresh, kv_len, slots, taken = _empty(2 * B + 2 + rows, torch.int32, block_table.device,
+                                                stream).split_with_sizes((B + 1, B, rows, 1))
+    else:
+        if cu_fresh is None or kv_len is None or slots is None or taken is None:
+            raise ValueError("give all of cu_fresh, kv_len, slots and taken, or none")
+        if cu_fresh.numel() != B + 1 or kv_len.numel() != B or slots.numel() != rows or taken.numel() != 1:
+            raise ValueError("cu_fresh is [B + 1], kv_len [B], slots [rows] and taken [1]")
+        given += [cu_fresh, kv_len, slots, taken]
     _int32(given, "cached, fresh, free_pages, cu_fresh, kv_len, slots and taken")
     index = block_table.get_device()
     _on_one_device(index, given)

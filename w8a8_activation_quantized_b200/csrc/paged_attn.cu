@@ -630,8 +630,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
 constexpr int kJoinThreads = 256;
 constexpr int kJoinPieces = 32;
 constexpr int kJoinSplit = 4;  // CTAs per record, each for a quarter of the dims
+constexpr int kJoinAhead = 2;  // pieces loaded before their weights are known
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads, 6) k_paged_join(const __grid_constant__ PagedAttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 5) k_paged_join(const __grid_constant__ PagedAttnArgs a) {
     constexpr int kQuads = D / 4 / kJoinSplit;  // groups of four dims per row
     static_assert(kRows * kQuads <= kJoinThreads, "four dims of a row per thread");
     __shared__ float2 s_ml[kJoinPieces][kRows];  // maximum and sum, then the weight
@@ -654,6 +655,13 @@ __global__ void __launch_bounds__(kJoinThreads, 6) k_paged_join(const __grid_con
     for (int p0 = 0; p0 < t.pieces; p0 += kJoinPieces) {
         const int np = min(kJoinPieces, t.pieces - p0);
         auto slot_of = [&](int i) { return p0 + i == 0 ? t.slot : 0; };
+        // the first pieces' sums are on their way while the weights are found
+        float4 y[kJoinAhead];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const int i = grp + k * groups;
+            if (grp < groups && i < np) y[k] = *reinterpret_cast<const float4*>(part_o<D>(a, c0 + p0 + i, slot_of(i)) + row * D + d4);
+        }
         __syncthreads();
         for (int x = threadIdx.x; x < np * kRows; x += kJoinThreads)
             if (x % kRows < t.rows) s_ml[x / kRows][x % kRows] = part_ml<D>(a, c0 + p0 + x / kRows, slot_of(x / kRows))[x % kRows];
@@ -679,15 +687,19 @@ __global__ void __launch_bounds__(kJoinThreads, 6) k_paged_join(const __grid_con
         if (grp < groups) {
             const float f = s_f[row];
             v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-#pragma unroll 4
-            for (int i = grp; i < np; i += groups) {
+            auto add = [&](int i, const float4& z) {
                 const float w = s_ml[i][row].x;
-                const float4 y = *reinterpret_cast<const float4*>(part_o<D>(a, c0 + p0 + i, slot_of(i)) + row * D + d4);
-                v.x = fmaf(y.x, w, v.x);
-                v.y = fmaf(y.y, w, v.y);
-                v.z = fmaf(y.z, w, v.z);
-                v.w = fmaf(y.w, w, v.w);
-            }
+                v.x = fmaf(z.x, w, v.x);
+                v.y = fmaf(z.y, w, v.y);
+                v.z = fmaf(z.z, w, v.z);
+                v.w = fmaf(z.w, w, v.w);
+            };
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k)
+                if (grp + k * groups < np) add(grp + k * groups, y[k]);
+#pragma unroll 2
+            for (int i = grp + kJoinAhead * groups; i < np; i += groups)
+                add(i, *reinterpret_cast<const float4*>(part_o<D>(a, c0 + p0 + i, slot_of(i)) + row * D + d4));
         }
     }
     s_sum[threadIdx.x] = v;

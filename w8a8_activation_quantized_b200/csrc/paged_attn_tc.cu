@@ -40,7 +40,7 @@
 // device: it lists the units longest first (each CTA takes them in snake
 // order, so the SMs finish together) and, when they are too few for the SMs,
 // cuts their key blocks into pieces whose fp32 results another kernel joins.
-// Every wait is bounded (mbar_wait).
+// Every wait is bounded (tile_wait).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -309,6 +309,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
 }
+// The waits of this kernel.  Their limit is longer than elsewhere, because a warp
+// in redo_row keeps the others waiting: 20 s, about two million keys of a unit.
+constexpr unsigned long long kTileWaitNs = 20000000000ull;
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort_flag) {
+    return mbar_wait_for(bar, parity, status, abort_flag, kTileWaitNs);
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t x;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
@@ -402,7 +409,9 @@ __device__ __forceinline__ float2* part_ml(const TcArgs& t, int slot, int row) {
 
 // One row of a unit on the CUDA cores, key by key: only the keys that this row
 // sees are touched.  Rare (see the top of the file), so it is simple: a first
-// pass over the keys for the maximum and the sum, then one per 64 dims.
+// pass over the keys for the maximum and the sum, then one per 64 dims.  It keeps
+// to few registers, which the tile kernel around it would otherwise spill, and
+// takes some 10 us per key of the unit.
 template <typename T, int D>
 __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const T* q, int pos, T* out,
                                       float* part, float2* ml) {
@@ -412,26 +421,30 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const
     const int32_t* table = a.table + u.b * a.ld_table;
     const T* kh = reinterpret_cast<const T*>(a.c.k) + head * a.c.sh;
     const T* vh = reinterpret_cast<const T*>(a.c.v) + head * a.c.sh;
+    constexpr int E = 64;
     float m = -INFINITY, l = 0.0f;
-    for (int pass = 0; pass <= D / 64; ++pass) {
-        float o[64];
+#pragma unroll 1
+    for (int pass = 0; pass <= D / E; ++pass) {
+        float o[E];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) o[i] = 0.0f;
+        for (int i = 0; i < E; ++i) o[i] = 0.0f;
         for (int vb = u.vb0; vb < u.vb0 + u.nblk; ++vb) {
             const int key0 = span.block(vb) * kKeys;
+            int page = -1;
             for (int key = key0; key < key0 + kKeys; ++key) {
-                if (!paged_sees(key, pos, a.window, a.sinks)) continue;
-                const int page = __ldg(table + (key >> a.c.ps_log2));
-                if (page < 0 || page >= a.c.num_pages) continue;
+                if ((key & 15) == 0) page = key <= pos ? __ldg(table + (key >> a.c.ps_log2)) : -1;  // pages hold 16 keys or more
+                if (page < 0 || page >= a.c.num_pages || !paged_sees(key, pos, a.window, a.sinks)) continue;
                 const int64_t off = page * a.c.sp + (key & (a.c.page_size - 1)) * a.c.st;
-                float s = 0.0f;
-                for (int d = 0; d < D; d += 8) {
+                float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+                for (int d = 0; d < D / 8; ++d) {
                     float x[8], y[8];
-                    unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(q + d)), x);
-                    unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(kh + off + d)), y);
+                    unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(q) + d), x);
+                    unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(kh + off) + d), y);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+                    for (int i = 0; i < 8; ++i) s4[i & 3] = fmaf(x[i], y[i], s4[i & 3]);
                 }
+                const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 if (pass == 0) {
                     const float mn = fmaxf(fmaxf(m, s), -FLT_MAX);
                     const float f = mn == m ? 1.0f : ex2((m - mn) * a.qscale);
@@ -439,13 +452,13 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const
                     m = mn;
                 } else {
                     const float p = ex2(fmaf(s, a.qscale, kOff<T> - m * a.qscale));
-                    const T* v = vh + off + (pass - 1) * 64;
+                    const uint4* v = reinterpret_cast<const uint4*>(vh + off + (pass - 1) * E);
 #pragma unroll
-                    for (int d = 0; d < 64; d += 8) {
+                    for (int d = 0; d < E / 8; ++d) {
                         float x[8];
-                        unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(v + d)), x);
+                        unpack8_f32<T>(__ldg(v + d), x);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) o[d + i] = fmaf(p, x[i], o[d + i]);
+                        for (int i = 0; i < 8; ++i) o[8 * d + i] = fmaf(p, x[i], o[8 * d + i]);
                     }
                 }
             }
@@ -456,11 +469,11 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const
         }
         const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < E; ++i) {
             if (part)
-                part[(pass - 1) * 64 + i] = o[i];
+                part[(pass - 1) * E + i] = o[i];
             else
-                out[(pass - 1) * 64 + i] = from_f32<T>(o[i] * inv);
+                out[(pass - 1) * E + i] = from_f32<T>(o[i] * inv);
         }
     }
 }
@@ -573,14 +586,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 if (keys) {  // posts the units to the other warps
                     while (r < rounds && !fetch(r, u)) ++r;
                     if (r++ >= rounds) u.nblk = -1;
-                    ok = mbar_wait(&uempty[n & 1], ((n >> 1) & 1) ^ 1, status, abort_flag);
+                    ok = tile_wait(&uempty[n & 1], ((n >> 1) & 1) ^ 1, status, abort_flag);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     if (lane == 0) {
                         s_unit[n & 1] = u;
                         mbar_arrive(&ufull[n & 1]);
                     }
                 } else {
-                    ok = mbar_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
+                    ok = tile_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     u = s_unit[n & 1];
                     __syncwarp();
@@ -620,7 +633,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     next = page_of(u.vb0 + i + 1);
                     const int st = keys ? blk % KS : blk % VS, ph = (keys ? blk / KS : blk / VS) & 1;
                     uint64_t* full = keys ? &kfull[st] : &vfull[st];
-                    ok = mbar_wait(keys ? &kempty[st] : &vempty[st], ph ^ 1, status, abort_flag);
+                    ok = tile_wait(keys ? &kempty[st] : &vempty[st], ph ^ 1, status, abort_flag);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     if (lane == 0) {
                         if (keys) s_lost[blk & 7] = lost;
@@ -638,7 +651,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     }
                     __syncwarp();
                     if (keys && i == 0) {  // the queries, once the last unit's products are done with theirs
-                        ok = mbar_wait(&qempty, (nq & 1) ^ 1, status, abort_flag);
+                        ok = tile_wait(&qempty, (nq & 1) ^ 1, status, abort_flag);
                         ok = __all_sync(0xffffffffu, ok);
                         const int tiles = u.ntok > t.tok ? 2 : 1;
                         const int bytes = t.tok * a.G * 128;
@@ -665,7 +678,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             int gb = 0, nq = 0, blk[2] = {0, 0};  // the rings' blocks and units so far, and the blocks of each tile
             bool ok = true;
             for (int n = 0; ok; ++n) {
-                ok = mbar_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
+                ok = tile_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const int nblk = s_unit[n & 1].nblk, tiles = s_unit[n & 1].ntok > t.tok ? 2 : 1;
                 __syncwarp();
@@ -683,7 +696,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                         umma_commit(&sfull[h]);
                     }
                 };
-                ok = mbar_wait(&kfull[gb % KS], (gb / KS) & 1, status, abort_flag) && mbar_wait(&qfull, nq & 1, status, abort_flag);
+                ok = tile_wait(&kfull[gb % KS], (gb / KS) & 1, status, abort_flag) && tile_wait(&qfull, nq & 1, status, abort_flag);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
                 // O_h (+)= P_h V of 64 keys, V in stage sv
@@ -699,7 +712,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 };
                 for (int h = 0; h < tiles && ok; ++h) {
                     if (kApart<D> && blk[h] > 0) {
-                        ok = mbar_wait(&sfree[h], (blk[h] - 1) & 1, status, abort_flag);
+                        ok = tile_wait(&sfree[h], (blk[h] - 1) & 1, status, abort_flag);
                         ok = __all_sync(0xffffffffu, ok);
                         tc_fence_after();
                     }
@@ -710,19 +723,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     const int sv = gb % VS, sk = (gb + 1) % KS;
                     const bool more = i + 1 < nblk;
                     if (kApart<D> && more) {  // the next scores first: they need only the last ones read
-                        ok = mbar_wait(&kfull[sk], ((gb + 1) / KS) & 1, status, abort_flag);
+                        ok = tile_wait(&kfull[sk], ((gb + 1) / KS) & 1, status, abort_flag);
                         for (int h = 0; h < tiles; ++h) {
-                            ok = ok && mbar_wait(&sfree[h], blk[h] & 1, status, abort_flag);
+                            ok = ok && tile_wait(&sfree[h], blk[h] & 1, status, abort_flag);
                             ok = __all_sync(0xffffffffu, ok);
                             tc_fence_after();
                             if (ok) scores(h, sk);
                         }
                     }
                     for (int h = 0; h < tiles; ++h) {
-                        if (h == 0) ok = ok && mbar_wait(&vfull[sv], (gb / VS) & 1, status, abort_flag);
+                        if (h == 0) ok = ok && tile_wait(&vfull[sv], (gb / VS) & 1, status, abort_flag);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            ok = ok && mbar_wait(&pfull[h][half], blk[h] & 1, status, abort_flag);
+                            ok = ok && tile_wait(&pfull[h][half], blk[h] & 1, status, abort_flag);
                             ok = __all_sync(0xffffffffu, ok);
                             tc_fence_after();
                             if (ok) values(h, half, sv, i == 0 && half == 0);
@@ -732,7 +745,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                         ++blk[h];
                         if (!kApart<D> && more) {
                             if (h == 0) {
-                                ok = mbar_wait(&kfull[sk], ((gb + 1) / KS) & 1, status, abort_flag);
+                                ok = tile_wait(&kfull[sk], ((gb + 1) / KS) & 1, status, abort_flag);
                                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                                 tc_fence_after();
                             }
@@ -757,7 +770,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
         int gb = 0;    // the rings' blocks before this unit
         bool ok = true;
         for (int n = 0;; ++n) {
-            if (ok) ok = mbar_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
+            if (ok) ok = tile_wait(&ufull[n & 1], (n >> 1) & 1, status, abort_flag);
             const TcUnit u = s_unit[n & 1];
             if (group_or(h, !ok || u.nblk < 0)) break;  // the group's warps go on, or end, together (and have read it)
             if (row == 0) mbar_arrive(&uempty[n & 1]);
@@ -786,7 +799,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             if (paired && h == 1 && lane == 0) mbar_arrive(other_turn);
             for (int i = 0; i < u.nblk; ++i, ++nb) {
                 const int key0 = span.block(u.vb0 + i) * kKeys;
-                ok = mbar_wait(&sfull[h], nb & 1, status, abort_flag);
+                ok = tile_wait(&sfull[h], nb & 1, status, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -804,7 +817,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 if (!whole) {
                     if (key0 + kKeys > u.len) {  // slots behind the request's end: V becomes zeros there
                         const int s = (gb + i) % VS;
-                        ok = mbar_wait(&vfull[s], ((gb + i) / VS) & 1, status, abort_flag);
+                        ok = tile_wait(&vfull[s], ((gb + i) / VS) & 1, status, abort_flag);
                         if (!__all_sync(0xffffffffu, ok)) {
                             ok = false;
                             break;
@@ -894,7 +907,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     l *= f;
                 }
                 if (kApart<D> && i > 0) {  // the last block's product is done: with P, and O is complete
-                    if (ok) ok = mbar_wait(&odone[h][(nb - 1) & 1], ((nb - 1) >> 1) & 1, status, abort_flag);
+                    if (ok) ok = tile_wait(&odone[h][(nb - 1) & 1], ((nb - 1) >> 1) & 1, status, abort_flag);
                     __syncwarp();
                     tc_fence_after();
                 }
@@ -927,7 +940,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 if constexpr (kApart<D>) {
                     uint32_t p[2][32];
                     if (paired) {
-                        if (ok) ok = mbar_wait(my_turn, turns++ & 1, status, abort_flag);
+                        if (ok) ok = tile_wait(my_turn, turns++ & 1, status, abort_flag);
                         __syncwarp();
                     }
                     weights(sr, p[0]);
@@ -966,8 +979,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             }
             gb += u.nblk;
             if (u.nblk > 0 && ok) {
-                ok = kApart<D> ? mbar_wait(&odone[h][(nb - 1) & 1], ((nb - 1) >> 1) & 1, status, abort_flag)
-                               : mbar_wait(&odone[h][0], nu & 1, status, abort_flag);
+                ok = kApart<D> ? tile_wait(&odone[h][(nb - 1) & 1], ((nb - 1) >> 1) & 1, status, abort_flag)
+                               : tile_wait(&odone[h][0], nu & 1, status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
                 for (int e = 0; !kApart<D> && e < frees; ++e) mbar_arrive(&vempty[(gb - 1) % VS]);
