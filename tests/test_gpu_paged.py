@@ -378,6 +378,163 @@ def test_captured_step_replays_with_other_lengths():
     cider.cider_device_status()
 
 
+def _reference(b):
+    """The float64 result on the GPU, request by request, laid out as the
+    oracle's (tests/test_gpu_paged.py holds the two together below)."""
+    T, H_q, D = b.q.shape
+    H_kv, ps = b.k.shape[1], b.page
+    G = H_q // H_kv
+    out = torch.full((T, H_q, D), float("nan"), dtype=torch.float64, device="cuda")
+    mag, smax = torch.zeros_like(out), torch.zeros((T, H_q), dtype=torch.float64, device="cuda")
+    cnt = torch.zeros(T, dtype=torch.int64, device="cuda")
+    at = 0
+    for r, (L, n) in enumerate(b.lens):
+        if n == 0:
+            continue
+        ids = b.table[r, :-(-L // ps)].long()
+        k = b.k[ids].transpose(1, 2).reshape(-1, H_kv, D)[:L].double()
+        v = b.v[ids].transpose(1, 2).reshape(-1, H_kv, D)[:L].double()
+        pos = torch.arange(L - n, L, device="cuda")[:, None]
+        j = torch.arange(L, device="cuda")[None, :]
+        see = j <= pos
+        if b.window:
+            see &= (j > pos - b.window) | (j < b.sinks)
+        for h in range(H_q):
+            q = b.q[at:at + n, h].double()
+            s = (b.scale * (q @ k[:, h // G].T)).masked_fill(~see, -float("inf"))
+            p = torch.softmax(s, -1)
+            out[at:at + n, h] = p @ v[:, h // G]
+            mag[at:at + n, h] = p @ v[:, h // G].abs()
+            smax[at:at + n, h] = (b.scale * (q.abs() @ k[:, h // G].abs().T)).masked_fill(~see, 0).amax(-1)
+        cnt[at:at + n] = see.sum(-1)
+        at += n
+    return [x.cpu().numpy() for x in (out, mag, smax, cnt)]
+
+
+def test_the_two_references_agree():
+    b = Batch([(130, 70), (33, 33), (260, 129)], 4, 2, D=64, page=32, seed=3, window=40, sinks=3)
+    for x, y in zip(_reference(b), b.oracle()):
+        np.testing.assert_allclose(x, y, rtol=1e-10, atol=1e-12)
+
+
+@pytest.mark.parametrize("D,page,dt", [(128, 16, "f16"), (128, 64, "bf16"), (64, 128, "f16"), (64, 16, "bf16")])
+@pytest.mark.parametrize("lens,window,sinks", [
+    ([(6000, 2500), (5000, 1900)], 0, 0),             # more units than SMs
+    ([(7001, 1500), (2000, 2000), (64, 1)], 900, 4),
+    ([(30000, 130)], 0, 0),                           # few units, cut into many pieces
+    ([(20000, 1), (1500, 700)], 0, 0),                # a long decode among chunks
+    ([(12000, 64)] * 9, 3000, 100),
+])
+def test_large_chunks(lens, window, sinks, D, page, dt):
+    b = Batch(lens, 16, 4, D=D, page=page, dt=dt, seed=D + page, window=window, sinks=sinks, pad=1)
+    check(b, b.run(cider), _reference(b))
+
+
+@pytest.mark.parametrize("lens", [[(9000, 1)] * 3, [(3000 + 37 * i, 1) for i in range(70)], [(17, 1)] * 900,
+                                  [(i % 40, i % 2) for i in range(4096)]])
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 1, 128), (4, 4, 64)])
+def test_large_decode_batches(lens, H_q, H_kv, D):
+    b = Batch(lens, H_q, H_kv, D=D, page=32, dt="bf16", seed=len(lens))
+    check(b, b.run(cider), _reference(b))
+
+
+@pytest.mark.parametrize("H_q,H_kv", [(130, 1), (256, 1), (34, 2), (128, 1)])
+def test_groups_of_more_heads_than_a_tile(H_q, H_kv):
+    b = Batch([(100, 3), (40, 33), (70, 1)], H_q, H_kv, D=64, seed=H_q)
+    check(b, b.run(cider))
+
+
+def test_padded_strides(kernel):
+    """Caches that are slices of wider ones, with strides that do not divide one
+    another, K and V interleaved page by page."""
+    for order in ("head", "token"):
+        b = Batch(LENS["chunks"], 6, 3, D=64, page=32, dt="f16", seed=12)
+        P, H, S, D = b.k.shape
+        if order == "head":
+            whole = torch.full((P, 2, H + 2, S + 3, D + 8), float("nan"), dtype=torch.float16, device="cuda")
+            k, v = whole[:, 0, :H, :S, :D], whole[:, 1, :H, :S, :D]
+        else:
+            whole = torch.full((P, 2, S + 3, H + 2, D + 8), float("nan"), dtype=torch.float16, device="cuda")
+            k, v = (whole[:, i, :S, :H, :D].transpose(1, 2) for i in (0, 1))
+        k.copy_(b.k)
+        v.copy_(b.v)
+        want = b.oracle()
+        b.k, b.v = k, v
+        check(b, b.run(cider), want)
+
+
+def test_captured_chunk_replays_with_other_lengths():
+    """A captured call whose lengths, table and queries change in place: chunks,
+    decode tokens and idle requests, whole and cut work lists."""
+    b = Batch([(3000, 600), (2500, 600)], 8, 2, seed=20, pad=50)
+    out = torch.zeros_like(b.q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        b.run(cider, out=out, max_fresh=b.T)
+    for lens in ([(3000, 600), (2500, 600)], [(3000, 1), (2500, 1)], [(100, 100), (2500, 1100)], [(0, 0), (17, 3)],
+                 [(0, 0), (0, 0)], [(2999, 1200), (1, 1)]):
+        b.lens = lens
+        b.kv_len.copy_(_i([L for L, _ in lens]))
+        b.cu.copy_(_i([0, lens[0][1], lens[0][1] + lens[1][1]]))
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(b, out, _reference(b))
+        assert (out[int(b.cu[-1]):] == 5).all()
+
+
+def test_two_captured_graphs_at_once():
+    """Each with its own workspace, replayed on two streams at the same time."""
+    bs = [Batch([(4000, 1)] * 5, 8, 2, seed=31), Batch([(1500, 400)], 8, 2, seed=32)]
+    want = [b.run(cider) for b in bs]
+    outs, graphs, streams = [torch.empty_like(w) for w in want], [], [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for b, o, s in zip(bs, outs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(5):
+                b.run(cider, out=o)
+        graphs.append(g)
+    for _ in range(10):
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("L,n", [(1000, 1000), (9000, 260)])
+def test_values_that_are_not_finite_reach_their_own_queries_alone(L, n):
+    """A NaN in the last token's V, an infinity in one in the middle of the chunk
+    (some of its dims): every query in front of them stays right, every element
+    behind them is what the formula says."""
+    b = Batch([(L, n)], 4, 2, D=128, page=64, seed=L)
+    mid = L - n // 2
+    for j, x in ((L - 1, float("nan")), (mid, float("inf"))):
+        b.v[int(b.table[0, j // 64]), :, j % 64, 5::9] = x
+    out = b.run(cider)
+    want, mag, smax, cnt = _reference(b)
+    got = out.double().cpu().numpy()
+    seen_inf = np.arange(n) >= n - n // 2
+    dims = np.zeros(128, dtype=bool)
+    dims[5::9] = True
+    # softmax in 64 bits gives 0 x inf = NaN where the mask gives weight 0: those are not the formula's
+    assert np.isfinite(got[~seen_inf]).all() and np.isfinite(got[:-1][:, :, ~dims]).all()
+    assert (got[seen_inf][:-1][:, :, dims] == np.inf).all() and np.isnan(got[-1][:, dims]).all()
+    b.v[int(b.table[0, (L - 1) // 64]), :, (L - 1) % 64, 5::9] = 0.0
+    b.v[int(b.table[0, mid // 64]), :, mid % 64, 5::9] = 0.0
+    clean = b.run(cider).double().cpu().numpy()
+    fine = np.isfinite(got)
+    # the same scores and weights; only the products' order differs (fp32 sums), then one rounding
+    assert np.abs(got - clean)[fine].max() <= 2.0 ** -10 * 2 * np.abs(clean).max() + 2 * L * 2.0 ** -24
+    cider.cider_device_status()
+
+
 def test_refusals_on_the_device():
     b = Batch([(40, 3)], 8, 2, seed=1)
     with pytest.raises(cider.CiderError):
