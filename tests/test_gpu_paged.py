@@ -545,3 +545,17 @@ def test_refusals_on_the_device():
         b.run(cider, out=torch.empty_like(b.q, device="cpu"))
     out = torch.empty((0, 8, 128), dtype=torch.float16, device="cuda")
     assert cider.cider_paged_attention(out, b.k, b.v, b.table, b.cu, b.kv_len).shape == (0, 8, 128)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_workspace_at_16_bytes_and_what_lies_behind_it(kernel, D):
+    """Units of several pieces, whose partial results the tensor-core kernel writes 32 bytes at a time."""
+    b = Batch([(3000, 64), (700, 3)], 8, 2, D=D, seed=11)
+    n = cider.cider_paged_attention_workspace_bytes(b.T, 2, 8, 2, D, b.max_fresh)
+    buf = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    assert buf.data_ptr() % 32 == 0
+    for at in (0, 16, 32):
+        check(b, b.run(cider, workspace=buf[at:at + n]))
+        torch.cuda.synchronize()
+        assert (buf[at + n:] == 0xA5).all()
+        buf.fill_(0xA5)

@@ -1123,7 +1123,7 @@ TcLayout tc_layout(int64_t T, int64_t B, int G, int D, int num_sms) {
     l.units = l.ranges + align256(grid * sizeof(int2));
     l.joins = l.units + align256((std::max<int64_t>(max_tiles(T, B, tok), kMaxCut) + grid) * sizeof(TcUnit));
     l.part = l.joins + align256(grid * sizeof(TcJoin));  // a cut unit ends at some CTA's share
-    l.total = l.part + slots * 256 * (D + 2) * sizeof(float);
+    l.total = l.part + slots * 256 * (D + 2) * sizeof(float) + 16;  // the workspace may begin 16 bytes before a multiple of 32
     return l;
 }
 
@@ -1142,7 +1142,7 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess || (e = cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev)) != cudaSuccess) return e;
     t.l2_keys = static_cast<int64_t>(l2) * 3 / 5 / (int64_t(4) * D * p.c.H_kv);
     const TcLayout l = tc_layout(p.T, p.B, p.G, D, num_sms);
-    char* ws = reinterpret_cast<char*>(p.part);
+    char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p.part) + 31) & ~uintptr_t(31));  // for store32
     t.plan = reinterpret_cast<TcPlan*>(ws);
     t.units = reinterpret_cast<TcUnit*>(ws + l.units);
     t.joins = reinterpret_cast<TcJoin*>(ws + l.joins);
