@@ -405,8 +405,10 @@ CIDER_API cider_status_t cider_paged_append(const cider_paged_cache_t* cache, co
  * window, sinks >= 0 and < 2^30; scale finite and > 0.
  * workspace: cider_paged_attention_workspace_bytes(...) bytes, 16-byte aligned.
  * In device memory, reported by cider_device_status(): cu_fresh outside [0, T]
- * or decreasing is cut to it; kv_len outside [0, width * page_size] is cut to
- * it; keys of a page outside [0, num_pages) count as not seen. */
+ * is cut to it; where it decreases, the request has no tokens, and rows that
+ * several requests then claim are not defined; kv_len outside [0, width *
+ * page_size] is cut to it; keys of a page outside [0, num_pages) count as not
+ * seen. */
 CIDER_API size_t cider_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t H_q, int64_t H_kv, int64_t D,
                                                        int64_t max_fresh);
 CIDER_API cider_status_t cider_paged_attention(const cider_paged_cache_t* cache, const void* q, int64_t ld_q, int64_t T,

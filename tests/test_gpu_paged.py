@@ -559,3 +559,22 @@ def test_workspace_at_16_bytes_and_what_lies_behind_it(kernel, D):
         torch.cuda.synchronize()
         assert (buf[at + n:] == 0xA5).all()
         buf.fill_(0xA5)
+
+
+def test_offsets_that_decrease_stay_inside_the_workspace(kernel):
+    """Every other request claims all rows: 2048 times as many blocks of queries as there are."""
+    T, B = 32768, 4096
+    b = Batch([(32, 1)] * B, 8, 2, D=64, page=32, seed=12, pad=T - B)
+    n = cider.cider_paged_attention_workspace_bytes(T, B, 8, 2, 64, T)
+    buf = torch.full((n + (32 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    cu = b.cu
+    b.cu = _i([0, T] * (B // 2) + [0])
+    out = torch.full((T + 64, 8, 64), 7.0, dtype=torch.float16, device="cuda")
+    b.run(cider, max_fresh=T, workspace=buf[:n], out=out[:T])
+    with pytest.raises(cider.CiderError) as e:
+        cider.cider_device_status()
+    assert e.value.status == 1
+    assert (buf[n:] == 0xA5).all() and (out[T:] == 7).all()
+    b.cu = cu
+    check(b, b.run(cider, max_fresh=T, workspace=buf[:n]))
+    cider.cider_device_status()

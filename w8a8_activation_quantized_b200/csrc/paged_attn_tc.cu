@@ -80,6 +80,7 @@ struct TcPlan {
 struct TcArgs {
     PagedAttnArgs p;
     int tok;              // tokens per 128-row tile: 128 / G
+    int max_tiles;        // records that the workspace holds: enough for offsets that do not decrease
     int boxes;            // pages per block (at least 1)
     int box_keys;         // keys per box: min(page_size, 128)
     int grid;
@@ -166,11 +167,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
     }
     if (any_bad) atomicOr(a.status, kStatusIndex);
     int64_t total;
-    const int base = static_cast<int>(block_prefix<kPlanThreads>(sum, s_warp, &total));
-    for (int b = b0; b < b1; ++b) pre[b] += base;
-    if (tid == 0) pre[a.B] = static_cast<int>(total);
+    const int64_t base = block_prefix<kPlanThreads>(sum, s_warp, &total);
+    for (int b = b0; b < b1; ++b) pre[b] = static_cast<int>(min(pre[b] + base, static_cast<int64_t>(INT_MAX)));
+    if (tid == 0) pre[a.B] = static_cast<int>(min(total, static_cast<int64_t>(INT_MAX)));
     __syncthreads();
-    const int tiles = static_cast<int>(total);
+    // Offsets that decrease can give the same rows to many requests; the list has
+    // room for each row once, and ends there.
+    const int tiles = static_cast<int>(min(total, static_cast<int64_t>(t.max_tiles)));
     auto unit = [&](int i) {
         TcUnit u;
         u.b = find_request(pre, a.B, i);
@@ -1132,6 +1135,7 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
     TcArgs t{};
     t.p = p;
     t.tok = 128 / p.G;
+    t.max_tiles = static_cast<int>(max_tiles(p.T, p.B, t.tok));
     t.box_keys = std::min(p.c.page_size, kKeys);
     t.boxes = kKeys / t.box_keys;
     t.grid = std::min(num_sms, kMaxGrid);
