@@ -578,3 +578,12 @@ def test_offsets_that_decrease_stay_inside_the_workspace(kernel):
     b.cu = cu
     check(b, b.run(cider, max_fresh=T, workspace=buf[:n]))
     cider.cider_device_status()
+
+
+def test_same_bits_with_blocks_beyond_the_planner_s_classes(kernel):
+    """More than 255 blocks of 128 keys: units of different lengths share a class of the sorted list."""
+    b = Batch([(40000, 70), (39900, 130), (39700, 64), (39500, 1), (20000, 65)], 4, 1, D=64, page=64, seed=13)
+    first = b.run(cider)
+    check(b, first)
+    for _ in range(10):
+        assert torch.equal(b.run(cider), first)

@@ -58,6 +58,7 @@ constexpr int kKeys = 128;                     // keys per block
 constexpr int kTcThreads = 384;                // warps 0-3: TMA, MMA, idle, TMA; then a softmax warpgroup per tile
 constexpr int kPlanThreads = 256;  // fewer threads, cheaper barriers: a prompt of 2048 52.8 us with 1024, 48.9 with 256
 constexpr int kMaxGrid = 256;                  // CTAs of the tile kernel: one per SM
+static_assert(kPlanThreads >= kMaxGrid, "the planner has a thread per CTA");
 constexpr int kMaxCut = 2560;                  // units up to which they may be cut
 constexpr int kMinShare = 2;                   // blocks per CTA where they are cut
 constexpr float kLazy = 8.0f;                  // log2 of the growth of a maximum that is put off
@@ -208,6 +209,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
     // whole: places by counting per class of length
     const float scale = (kPlanThreads - 1.0f) / max(1, mx);
     auto bin = [&](int n) { return kPlanThreads - 1 - min(kPlanThreads - 1, static_cast<int>(n * scale)); };
+    // A class's length (rounded up; where a class holds one length, that).  The units of
+    // a class come in any order, and what is chosen below may not depend on it.
+    auto length = [&](int bin) { return ((kPlanThreads - 1 - bin) * mx + kPlanThreads - 2) / (kPlanThreads - 1); };
     for (int i = i0; i < i1; ++i) atomicAdd(&s_hist[bin(unit(i).nblk)], 1);
     __syncthreads();
     const int64_t place = block_prefix<kPlanThreads>(s_hist[tid], s_warp, &total);
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
         const TcUnit u = unit(i);
         const int at = atomicAdd(&s_hist[bin(u.nblk)], 1);
         t.units[at] = u;
-        if (may_cut) s_sorted[at] = u.nblk;
+        if (may_cut) s_sorted[at] = length(bin(u.nblk));
     }
     __syncthreads();
     work *= a.c.H_kv;
@@ -1169,9 +1173,9 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
     const int plan_smem = (4 * p.B + 1) * 4;
     if ((e = cudaFuncSetAttribute(k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_smem)) != cudaSuccess) return e;
     if ((e = launch_pdl(k_paged_plan, dim3(1), dim3(kPlanThreads), plan_smem, st, t)) != cudaSuccess) return e;
-    if ((e = launch_pdl(kern, dim3(num_sms), dim3(kTcThreads), smem, st, tmQ, tmK, tmV, t)) != cudaSuccess) return e;
+    if ((e = launch_pdl(kern, dim3(t.grid), dim3(kTcThreads), smem, st, tmQ, tmK, tmV, t)) != cudaSuccess) return e;
     // as many CTAs as are resident: a row is a few dependent loads
-    return launch_pdl(k_paged_tc_join<T, D>, dim3(6 * num_sms), dim3(256), 0, st, t);
+    return launch_pdl(k_paged_tc_join<T, D>, dim3(6 * t.grid), dim3(256), 0, st, t);
 }
 
 }  // namespace
