@@ -402,8 +402,11 @@ CIDER_API cider_status_t cider_paged_append(const cider_paged_cache_t* cache, co
  * as they are.  max_fresh: a bound on the new tokens of any one request (T is
  * always one), by which the kernel is chosen; a bound that does not hold costs
  * time, not correctness.  0 <= T <= 2^30 / (H_q / H_kv); 1 <= B <= 4096;
- * window, sinks >= 0 and < 2^30; scale finite and > 0.
- * workspace: cider_paged_attention_workspace_bytes(...) bytes, 16-byte aligned.
+ * window, sinks >= 0 and < 2^30; scale > 0 and finite, times log2(e) too.
+ * workspace: cider_paged_attention_workspace_bytes(...) bytes, 16-byte aligned;
+ * calls that may run at the same time need one each.
+ * A value in V that is not finite costs time: in the chunks' kernel the rows of
+ * its block of queries are computed again key by key (about 10 us per key).
  * In device memory, reported by cider_device_status(): cu_fresh outside [0, T]
  * is cut to it; where it decreases, the request has no tokens, and rows that
  * several requests then claim are not defined; kv_len outside [0, width *

@@ -143,3 +143,8 @@ def test_the_binding_refuses_what_the_abi_cannot_see():
         with pytest.raises(ValueError):
             c()
             pytest.fail(f"case {n} was taken")
+
+
+def test_a_scale_that_overflows_in_base_two_is_refused(lib):
+    assert _attend(lib, scale=3.0e38) == 1  # finite, but 3e38 log2(e) is not
+    assert b"log2" in lib.cider_last_error()

@@ -923,7 +923,9 @@ cider_status_t cider_paged_attention(const cider_paged_cache_t* cache, const voi
                     (long long)width, (long long)ld_table);
     if (window < 0 || window >= kMaxLen || sinks < 0 || sinks >= kMaxLen)
         return fail(CIDER_ERR_INVALID_ARG, "window = %lld and sinks = %lld must lie in [0, 2^30)", (long long)window, (long long)sinks);
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(CIDER_ERR_INVALID_ARG, "scale = %g must be finite and > 0", scale);
+    const float qscale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // log2(e)
+    if (!(scale > 0.0f) || !std::isfinite(qscale))
+        return fail(CIDER_ERR_INVALID_ARG, "scale = %g must be > 0, and finite times log2(e)", scale);
     if (T == 0) return CIDER_OK;
     if (!q || !out || !cu_fresh || !kv_len || !block_table || !workspace) return fail(CIDER_ERR_INVALID_ARG, "NULL pointer");
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
@@ -956,7 +958,7 @@ cider_status_t cider_paged_attention(const cider_paged_cache_t* cache, const voi
     a.width = static_cast<int>(width);
     a.window = static_cast<int>(window);
     a.sinks = static_cast<int>(sinks);
-    a.qscale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.qscale = qscale;
     a.out = out;
     a.ld_out = T > 1 ? ld_out : row;
     a.part = static_cast<float*>(workspace);
