@@ -29,7 +29,7 @@
 //    weights.  Other rows of V are tokens' values: finite, as a rule.  If one that
 //    some query does not see is not, 0 x V makes that query's output NaN; a row
 //    whose output is not finite although its weights' sum is gets computed again
-//    key by key (redo_row), from the keys that it sees alone.
+//    by its warp (redo_row), from the keys that it sees alone.
 //
 // What bounds it: per 128 x 128 block of scores the two products take 1024
 // cycles of the tensor pipe at D = 128 (8192 fp16 operations per cycle and SM),
@@ -317,7 +317,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         : "memory");
 }
 // The waits of this kernel.  Their limit is longer than elsewhere, because a warp
-// in redo_row keeps the others waiting: 20 s, about two million keys of a unit.
+// in redo_row keeps the others waiting: 20 s, some ten million keys of a unit.
 constexpr unsigned long long kTileWaitNs = 20000000000ull;
 __device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort_flag) {
     return mbar_wait_for(bar, parity, status, abort_flag, kTileWaitNs);
@@ -414,74 +414,78 @@ __device__ __forceinline__ float2* part_ml(const TcArgs& t, int slot, int row) {
     return reinterpret_cast<float2*>(t.part + static_cast<int64_t>(t.slots) * 256 * D) + static_cast<int64_t>(slot) * 256 + row;
 }
 
-// One row of a unit on the CUDA cores, key by key: only the keys that this row
-// sees are touched.  Rare (see the top of the file), so it is simple: a first
-// pass over the keys for the maximum and the sum, then one per 64 dims.  It keeps
-// to few registers, which the tile kernel around it would otherwise spill, and
-// takes some 10 us per key of the unit.
+// One row of a unit on the CUDA cores, by one warp: each lane has D / 32 dims, 16
+// keys (of one page) at a time, and only keys that the row sees reach the result.
+// Rare (see the top of the file).  It keeps to few registers, which the tile
+// kernel around it would otherwise spill.  A warp whose 32 rows all need it takes
+// 1 to 2 us per key of the unit (a prompt of 2048 with NaN everywhere: 4 ms).
 template <typename T, int D>
-__device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int head, const T* q, int pos, T* out,
-                                      float* part, float2* ml) {
+__device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int row) {
+    constexpr int E = D / 32, N = 16;
+    using Vec = std::conditional_t<E == 4, uint2, uint32_t>;
     const PagedAttnArgs& a = t.p;
+    const int lane = threadIdx.x & 31;
+    const int tok = (row >> 7) * t.tok + (row & 127) / a.G, pos = u.pmin + tok;
+    const int64_t q_row = u.token0 + tok, col = static_cast<int64_t>(u.head * a.G + (row & 127) % a.G) * D + lane * E;
     PagedSpan<kKeys> span;
     span.set(u.pmin, u.pmin + u.ntok - 1, a.window, a.sinks);
     const int32_t* table = a.table + u.b * a.ld_table;
-    const T* kh = reinterpret_cast<const T*>(a.c.k) + head * a.c.sh;
-    const T* vh = reinterpret_cast<const T*>(a.c.v) + head * a.c.sh;
-    constexpr int E = 64;
-    float m = -INFINITY, l = 0.0f;
-#pragma unroll 1
-    for (int pass = 0; pass <= D / E; ++pass) {
-        float o[E];
+    const T* kh = reinterpret_cast<const T*>(a.c.k) + u.head * a.c.sh + lane * E;
+    const T* vh = reinterpret_cast<const T*>(a.c.v) + u.head * a.c.sh + lane * E;
+    auto load = [](const T* p) { return __ldg(reinterpret_cast<const Vec*>(p)); };
+    float q[E], o[E], m = -INFINITY, l = 0.0f;
+    const Vec qv = load(static_cast<const T*>(a.q) + q_row * a.ld_q + col);
 #pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = 0.0f;
-        for (int vb = u.vb0; vb < u.vb0 + u.nblk; ++vb) {
-            const int key0 = span.block(vb) * kKeys;
-            int page = -1;
-            for (int key = key0; key < key0 + kKeys; ++key) {
-                if ((key & 15) == 0) page = key <= pos ? __ldg(table + (key >> a.c.ps_log2)) : -1;  // pages hold 16 keys or more
-                if (page < 0 || page >= a.c.num_pages || !paged_sees(key, pos, a.window, a.sinks)) continue;
-                const int64_t off = page * a.c.sp + (key & (a.c.page_size - 1)) * a.c.st;
-                float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-                for (int d = 0; d < D / 8; ++d) {
-                    float x[8], y[8];
-                    unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(q) + d), x);
-                    unpack8_f32<T>(__ldg(reinterpret_cast<const uint4*>(kh + off) + d), y);
+    for (int e = 0; e < E; ++e) {
+        q[e] = to_f32<T>(reinterpret_cast<const T*>(&qv)[e]);
+        o[e] = 0.0f;
+    }
+    for (int vb = u.vb0; vb < u.vb0 + u.nblk; ++vb) {
+        const int block = span.block(vb) * kKeys;
+        for (int key0 = block; key0 < block + kKeys && key0 <= pos; key0 += N) {  // pages hold 16 keys or more
+            const int page = __ldg(table + (key0 >> a.c.ps_log2));
+            if (page < 0 || page >= a.c.num_pages) continue;
+            const int64_t off = page * a.c.sp + (key0 & (a.c.page_size - 1)) * a.c.st;
+            Vec k[N], v[N];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s4[i & 3] = fmaf(x[i], y[i], s4[i & 3]);
-                }
-                const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                if (pass == 0) {
-                    const float mn = fmaxf(fmaxf(m, s), -FLT_MAX);
-                    const float f = mn == m ? 1.0f : ex2((m - mn) * a.qscale);
-                    l = l * f + ex2(fmaf(s, a.qscale, kOff<T> - mn * a.qscale));
-                    m = mn;
-                } else {
-                    const float p = ex2(fmaf(s, a.qscale, kOff<T> - m * a.qscale));
-                    const uint4* v = reinterpret_cast<const uint4*>(vh + off + (pass - 1) * E);
+            for (int i = 0; i < N; ++i) k[i] = load(kh + off + i * a.c.st);
 #pragma unroll
-                    for (int d = 0; d < E / 8; ++d) {
-                        float x[8];
-                        unpack8_f32<T>(__ldg(v + d), x);
+            for (int i = 0; i < N; ++i) v[i] = load(vh + off + i * a.c.st);
+            float s[N], mn = m;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) o[8 * d + i] = fmaf(p, x[i], o[8 * d + i]);
-                    }
-                }
+            for (int i = 0; i < N; ++i) {
+                s[i] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[i] = fmaf(q[e], to_f32<T>(reinterpret_cast<const T*>(&k[i])[e]), s[i]);
+#pragma unroll
+                for (int w = 16; w > 0; w >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], w);
+                if (paged_sees(key0 + i, pos, a.window, a.sinks)) mn = fmaxf(fmaxf(mn, s[i]), -FLT_MAX);
+            }
+            const float f = mn == m ? 1.0f : ex2((m - mn) * a.qscale), ms = kOff<T> - mn * a.qscale;
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (!paged_sees(key0 + i, pos, a.window, a.sinks)) continue;
+                const float p = ex2(fmaf(s[i], a.qscale, ms));
+                l += p;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(p, to_f32<T>(reinterpret_cast<const T*>(&v[i])[e]), o[e]);
             }
         }
-        if (pass == 0) {
-            if (ml) *ml = make_float2(m, l);
-            continue;
-        }
-        const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+    }
+    if (u.slot >= 0) {
+        float* part = part_row<D>(t, u.slot, row) + lane * E;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (part)
-                part[(pass - 1) * E + i] = o[i];
-            else
-                out[(pass - 1) * E + i] = from_f32<T>(o[i] * inv);
-        }
+        for (int e = 0; e < E; ++e) part[e] = o[e];
+        if (lane == 0) *part_ml<D>(t, u.slot, row) = make_float2(m, l);
+    } else {
+        const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+        T* out = static_cast<T*>(a.out) + q_row * a.ld_out + col;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack2<T>(o[e] * inv, o[e + 1] * inv);
     }
 }
 
@@ -1035,10 +1039,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
             }
             // NaN or an infinity in O although the weights' sum is finite: it came from V,
             // perhaps from a row of it that this query does not see.
-            if (odd && live && l < INFINITY)
-                redo_row<T, D>(t, u, head, static_cast<const T*>(a.q) + q_row * a.ld_q + q_col, pos, out,
-                               slot >= 0 ? part_row<D>(t, slot, h * 128 + row) : nullptr,
-                               slot >= 0 ? part_ml<D>(t, slot, h * 128 + row) : nullptr);
+            for (uint32_t rows = __ballot_sync(0xffffffffu, odd && live && l < INFINITY); rows; rows &= rows - 1) {
+                __syncwarp();  // its lane's stores are overwritten
+                redo_row<T, D>(t, u, h * 128 + (warp & 3) * 32 + __ffs(rows) - 1);
+            }
             tc_fence_before();
         }
     }
