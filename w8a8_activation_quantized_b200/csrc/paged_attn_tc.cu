@@ -837,41 +837,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                             if (key0 + ((e >> 3) & (kKeys - 1)) >= u.len) reinterpret_cast<uint4*>(sV + s * TB)[e] = make_uint4(0, 0, 0, 0);
                         fence_async_smem();
                     }
-                    // S: -inf where the row does not see the key, 64 columns at a
-                    // time and back to tensor memory, so that the registers hold
-                    // the 128 scores only once (a spill goes to L2: shared memory
-                    // leaves no L1)
+                    // S: -inf where the row does not see the key, 32 columns at a time
+                    // and back to tensor memory, so that the registers hold the 128
+                    // scores only once (a spill goes to L2: shared memory leaves no L1).
+                    // Columns that all rows of the warp see stay as they are, and those
+                    // that none sees are not read: of a block on the diagonal or at a
+                    // window's start three of the four chunks are one or the other.
                     const int last = pos - key0;                                             // seen: x <= last
                     const int first = a.window > 0 ? max(pos - a.window, -1) - key0 : -1;    // and x > first
                     const int sink = a.window > 0 ? max(min(a.sinks - key0, kKeys), 0) : 0;  // or x < sink
                     uint32_t any = 0;
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t x[2][32];
-                        tmem_ld_32x32b_x32(tS + half * 64, x[0]);
-                        tmem_ld_32x32b_x32(tS + half * 64 + 32, x[1]);
-                        uint32_t see[2];  // the row's seen columns as bits
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int lo = half * 64 + c * 32;
-                            const uint32_t below = last - lo >= 31 ? ~0u : last < lo ? 0u : (2u << (last - lo)) - 1;
-                            const uint32_t after = first < lo ? ~0u : first - lo >= 31 ? 0u : ~((2u << (first - lo)) - 1);
-                            const uint32_t sinks = sink <= lo ? 0u : sink - lo >= 32 ? ~0u : (1u << (sink - lo)) - 1;
-                            see[c] = below & (after | sinks);
-                            if (lost)
-                                for (int e = 0; e < 32; e += 16)  // pages hold 16 keys or more
-                                    if ((lost >> ((lo + e) / t.box_keys)) & 1u) see[c] &= ~(0xffffu << e);
-                            any |= see[c];
-                        }
-                        ld_wait(x[0]);
-                        ld_wait(x[1]);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < 4; ++c) {
+                        const int lo = c * 32;
+                        const uint32_t below = last - lo >= 31 ? ~0u : last < lo ? 0u : (2u << (last - lo)) - 1;
+                        const uint32_t after = first < lo ? ~0u : first - lo >= 31 ? 0u : ~((2u << (first - lo)) - 1);
+                        const uint32_t sinks = sink <= lo ? 0u : sink - lo >= 32 ? ~0u : (1u << (sink - lo)) - 1;
+                        uint32_t see = below & (after | sinks);  // the row's seen columns as bits
+                        if (lost)
+                            for (int e = 0; e < 32; e += 16)  // pages hold 16 keys or more
+                                if ((lost >> ((lo + e) / t.box_keys)) & 1u) see &= ~(0xffffu << e);
+                        any |= see;
+                        if (__all_sync(0xffffffffu, see == ~0u)) continue;
+                        uint32_t x[32];
+                        if (__any_sync(0xffffffffu, see)) {
+                            tmem_ld_32x32b_x32(tS + lo, x);
+                            ld_wait(x);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!((see[c] >> e) & 1u)) x[c][e] = 0xff800000u;  // -inf
-                            tmem_st_32x32b_x32(tS + half * 64 + c * 32, x[c]);
+                                if (!((see >> e) & 1u)) x[e] = 0xff800000u;  // -inf
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = 0xff800000u;
                         }
+                        tmem_st_32x32b_x32(tS + lo, x);
                     }
                     tmem_st_wait();
                     if (!any) low = -INFINITY;
