@@ -400,8 +400,8 @@ CIDER_API cider_status_t cider_paged_append(const cider_paged_cache_t* cache, co
  * q: T rows of [H_q][D] at row stride ld_q; out: the same at ld_out (multiples
  * of 8, at least H_q * D for T > 1); rows of out behind cu_fresh[B] are left
  * as they are.  max_fresh: a bound on the new tokens of any one request (T is
- * always one), by which the kernel is chosen; a bound that does not hold costs
- * time, not correctness.  0 <= T <= 2^30 / (H_q / H_kv); 1 <= B <= 4096;
+ * always one), by which, with the table's width, the kernel is chosen; a bound
+ * that does not hold costs time, not correctness.  0 <= T <= 2^30 / (H_q / H_kv); 1 <= B <= 4096;
  * window, sinks >= 0 and < 2^30; scale > 0 and finite, times log2(e) too.
  * workspace: cider_paged_attention_workspace_bytes(...) bytes, 16-byte aligned;
  * calls that may run at the same time need one each.

@@ -587,3 +587,15 @@ def test_same_bits_with_blocks_beyond_the_planner_s_classes(kernel):
     check(b, first)
     for _ in range(10):
         assert torch.equal(b.run(cider), first)
+
+
+@pytest.mark.parametrize("D,H_q,H_kv", [(128, 32, 8), (64, 16, 2)])
+@pytest.mark.parametrize("B,n", [(1, 5), (1, 16), (1, 40), (6, 9), (16, 5)])
+def test_the_table_s_width_chooses_a_kernel_and_changes_no_result(B, n, D, H_q, H_kv):
+    """A wide table is a large bound on the keys: the tensor-core tiles; a tight one may mean the 16-row tiles."""
+    b = Batch([(700 + 37 * i, max(1, n - i)) for i in range(B)], H_q, H_kv, D=D, page=32, seed=14 + n)
+    check(b, b.run(cider))
+    wide = torch.full((B, 4096), -7, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    check(b, b.run(cider))

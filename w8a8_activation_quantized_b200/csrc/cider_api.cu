@@ -809,12 +809,29 @@ cider_status_t check_cache(const cider_paged_cache_t* c, PagedCache* out, size_t
     return CIDER_OK;
 }
 
-// Whether a call runs on the tensor-core tiles: when a request may bring more
-// rows than one 16-row tile holds.
-bool paged_on_tc(int64_t G, int64_t max_fresh, int64_t T) {
+// Whether a call may run on the tensor-core tiles: when a request may bring more
+// rows than one 16-row tile holds (16 requests of 4096 keys, 32 / 8 heads, D = 128:
+// 16 rows 54.7 us in 16-row tiles, 70.9 in the others; 20 rows 79.1 and 70.4; 64
+// rows 173 and 70.7).
+bool paged_may_tc(int64_t G, int64_t max_fresh, int64_t T) {
     const int forced = g_paged_kernel.load();
     if (forced == 1 || !paged_tc_applies(static_cast<int>(G))) return false;
     return forced == 2 || std::min(max_fresh, T) * G > 16;
+}
+
+// Whether it does.  The 16-row kernel is about 10 us shorter where there is little
+// to do (no work list, smaller tiles): per 64 keys and KV head it takes 0.7 us of an
+// SM (D = 64: 0.46) for each tile of a request's rows, the other one 1.0 (0.88) for
+// all of them.  The keys are bounded by the table's width, which is what the host
+// knows.  One request of 4096 keys, 32 / 8 heads, D = 128: 20 rows 18.0 and 28.1 us,
+// 64 rows 23.1 and 29.6, 128 rows 30.7 and 30.9.  64 requests, 32 / 4 heads, D = 64:
+// 32 rows 107 and 112, 64 rows 197 and 112.
+bool paged_on_tc(int64_t G, int64_t max_fresh, int64_t T, int64_t B, int64_t H_kv, int64_t D, int64_t table_keys, int num_sms) {
+    if (!paged_may_tc(G, max_fresh, T)) return false;
+    if (g_paged_kernel.load() == 2) return true;
+    const double tiles = static_cast<double>((std::min(max_fresh, T) * G + 15) / 16);
+    const double more = D == 128 ? 0.7 * tiles - 1.0 : 0.46 * tiles - 0.88;
+    return more * static_cast<double>(B * H_kv) * (static_cast<double>(table_keys) / 64) > 10.0 * num_sms;
 }
 
 cider_status_t check_paged_attn(int64_t T, int64_t B, int64_t H_q, int64_t H_kv, int64_t D, int64_t max_fresh) {
@@ -900,8 +917,9 @@ size_t cider_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t H_q, 
     DeviceInfo* d = nullptr;
     if (device_info(&d) != CIDER_OK) return 0;
     const int G = static_cast<int>(H_q / H_kv);
-    if (paged_on_tc(G, max_fresh, T)) return paged_tc_bytes(T, B, G, static_cast<int>(D), d->num_sms);
-    return paged_rows16_bytes(static_cast<int>(D), d->num_sms);
+    const size_t rows16 = paged_rows16_bytes(static_cast<int>(D), d->num_sms);  // what either kernel takes
+    if (!paged_may_tc(G, max_fresh, T)) return rows16;
+    return std::max(rows16, paged_tc_bytes(T, B, G, static_cast<int>(D), d->num_sms));
 }
 
 cider_status_t cider_paged_attention(const cider_paged_cache_t* cache, const void* q, int64_t ld_q, int64_t T, int64_t H_q,
@@ -964,7 +982,8 @@ cider_status_t cider_paged_attention(const cider_paged_cache_t* cache, const voi
     a.part = static_cast<float*>(workspace);
     a.status = d->status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = paged_on_tc(a.G, max_fresh, T) ? launch_paged_tc(a, d->num_sms, st) : launch_paged_rows16(a, d->num_sms, st);
+    const bool tc = paged_on_tc(a.G, max_fresh, T, B, cache->H_kv, cache->D, width * cache->page_size, d->num_sms);
+    cudaError_t e = tc ? launch_paged_tc(a, d->num_sms, st) : launch_paged_rows16(a, d->num_sms, st);
     return e == cudaSuccess ? CIDER_OK : cuda_fail(e, "paged-attention launch");
 }
 

@@ -19,7 +19,8 @@
 // that use them, each 16 keys of a block, and on into the next tile; two CTAs
 // per SM keep up to 192 KB in flight.  (The using warps' instructions set the
 // pace where the bytes do not: with 16-byte cp.async of their own, and with TMA
-// of their own, four requests of up to 32K keys took 49.5 and 45.2 us.)  Pages that
+// of their own, four requests of up to 32K keys took 49.5 and 45.2 us, with this
+// warp 41.)  Pages that
 // no query of the tile sees are not read; their boxes lie outside the tensor
 // map, which makes them zeros.  Where only some keys of a step are seen by any
 // query, the other rows of V are zeroed in shared memory: what the cache's
@@ -34,6 +35,12 @@
 // workspace (the first piece of its share, or the last), and a second kernel
 // joins the pieces.  The lengths are in device memory, so every CTA computes
 // the line's prefix sums over the requests by itself.
+//
+// Measured (with the join, calls back to back): 64 requests of up to 8K keys, 32 / 8
+// heads, D = 128: 208 to 212 us, 6.4 to 6.5 TB/s, the rate of a copy; 4 of up to
+// 32K, 32 / 4 heads: 41 to 43 us, of which the 176 MB are 27 and the start and the
+// join the rest; 16 windows of 4096 keys, 32 / 32 heads, D = 64: 96 us, 5.6 TB/s;
+// one request of 1000 keys: 11.3 us, the two launches' chains of loads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -55,8 +62,8 @@ constexpr int kBlock = kWarps * kStep;  // keys per block of the line
 template <int D>
 constexpr int kRing = D == 128 ? 3 : 6;  // blocks in the ring: 96 KB
 constexpr int kCtasPerSm = 2;
-// Shortest share of a CTA, in blocks: below it the pieces' join costs more
-// than the parallelism gains.
+// Shortest share of a CTA, in blocks: with 2 or 3 there would be fewer pieces to
+// join, but one short request (1000 keys) and four long ones were slower.
 constexpr int kMinShare = 1;
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, PTX ex2.approx (relative error near 2^-22)
@@ -398,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
                 for (int hh = 0; hh < 2; ++hh) pos[hh] = t.r.L - t.r.n + (t.row0 + g + 8 * hh) / a.G;
             }
             // The queries stay in shared memory at D = 128: in registers, 32, they
-            // would spill others (four requests of up to 32K keys: 49.0 -> 46.3 us).
+            // would spill others (four requests of up to 32K keys, when that was tried: 49.0
+            // and 46.3 us).
             const uint32_t q_row = smem_u32(s_q[buf]) + q_off;
             uint32_t q[kNd][4];
             if (D == 64)
@@ -626,7 +634,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
 // out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M), kJoinPieces at a time.  A
 // tile may have as many pieces as there are CTAs, so the threads that a tile's
 // rows leave over share the pieces.  A CTA is small enough (registers, shared
-// memory) to be resident beside two of the kernel before it, and waits there.
+// memory) to be resident beside two of the kernel before it, and waits there: 8.4
+// us by itself, about 4 behind that kernel.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinPieces = 32;
 constexpr int kJoinSplit = 4;  // CTAs per record, each for a quarter of the dims
