@@ -599,3 +599,16 @@ def test_the_table_s_width_chooses_a_kernel_and_changes_no_result(B, n, D, H_q, 
     wide[:, :b.table.shape[1]] = b.table
     b.table = wide
     check(b, b.run(cider))
+
+
+@pytest.mark.parametrize("lens", [[(2048, 2048)], [(500, 500), (1200, 1200), (3000, 3000), (200, 200)], [(300, 300), (9000, 64), (70, 70), (5, 5), (0, 0)],
+                                  [(60, 100), (6000, 40), (40, 200)]])
+@pytest.mark.parametrize("D,H_q,H_kv", [(128, 8, 2), (64, 8, 1), (128, 4, 4)])
+def test_units_of_all_lengths_on_one_line(lens, D, H_q, H_kv):
+    """Short and long units side by side, cut into equal shares; some that see nothing among them."""
+    cider.cider_test_set_paged_kernel(2)
+    try:
+        b = Batch(lens, H_q, H_kv, D=D, page=16, seed=15)
+        check(b, b.run(cider))
+    finally:
+        cider.cider_test_set_paged_kernel(0)

@@ -68,7 +68,8 @@ constexpr int kPlanThreads = 256;  // fewer threads, cheaper barriers: a prompt 
 constexpr int kMaxGrid = 256;                  // CTAs of the tile kernel: one per SM
 static_assert(kPlanThreads >= kMaxGrid, "the planner has a thread per CTA");
 constexpr int kMaxCut = 2560;                  // units up to which they may be cut
-constexpr int kMinShare = 2;                   // blocks per CTA where they are cut
+constexpr int kUnitCost = 2;                   // the start and end of a unit, in blocks
+constexpr int kMinShare = 2 + kUnitCost;       // length per CTA where the line is cut
 constexpr float kLazy = 8.0f;                  // log2 of the growth of a maximum that is put off
 
 // One unit: tokens [token0, token0 + ntok) of q's rows, the first at position
@@ -125,12 +126,14 @@ __device__ __forceinline__ int span_blocks(const PagedAttnArgs& a, int pmin, int
 }
 
 // Two ways to share the units out.  Whole: the list is sorted, longest first,
-// and each CTA takes its units in snake order.  Cut: the units' blocks form one
-// line, in order, of which each CTA takes an equal share; a unit that several
-// share leaves fp32 partial results, at most two per CTA, for the join.  The
-// cheaper one is taken, in blocks: whole, the longest CTA; cut, the share, the
-// start and end of a unit (about two blocks each) once more per CTA, and eight
-// for writing and joining the partial results.  With units for every SM the cut
+// and each CTA takes its units in snake order.  Cut: the units form one line, in
+// order, each as long as its blocks and kUnitCost (half in front, half behind), of
+// which each CTA takes an equal share; a unit that several share leaves fp32 partial
+// results, at most two per CTA, for the join.  (With the blocks alone the CTA with
+// the first, short tiles of a prompt got many of them: 4096 tokens, 8 / 2 heads, 79
+// us; now 58, and whole units 73.)  The cheaper one is taken, in blocks: whole, the
+// longest CTA; cut, the share, the start and end of a unit once more per CTA, and
+// eight for writing and joining the partial results.  With units for every SM the cut
 // also needs the keys and values to stay in the L2: whole units of the same
 // head walk through its keys together and read them from HBM once, the cut ones
 // start all over the place (four chunks of 500 over 268 MB of keys and values:
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
     for (int i = i0; i < i1; ++i) {
         const int n = unit(i).nblk;
         mx = max(mx, n);
-        blocks += n;
+        blocks += n + kUnitCost;
     }
     mx = __reduce_max_sync(0xffffffffu, mx);
     if (lane == 0) atomicMax(&s_max, mx);
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
         if (tid < t.grid)
             for (int r = 0; r * t.grid < units; ++r) {
                 const int x = r * t.grid + ((r & 1) ? t.grid - 1 - tid : tid);
-                if (x < units) load += s_sorted[x / a.c.H_kv] + 2;
+                if (x < units) load += s_sorted[x / a.c.H_kv] + kUnitCost;
             }
         load = __reduce_max_sync(0xffffffffu, load);
         __syncthreads();
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
         __syncthreads();
         if (lane == 0) atomicMax(&s_max, load);
         __syncthreads();
-        cut = share + 2 * ((units + t.grid - 1) / t.grid + 1) + 8 < s_max &&
+        cut = share + kUnitCost + 8 < s_max &&
               (units < t.grid || static_cast<int64_t>(s_keys) <= t.l2_keys);
     }
     if (cut) {
@@ -259,17 +262,23 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
         for (int i = i0; i < i1; ++i) {
             TcUnit u = unit(i);
             const int n = u.nblk;
+            const int w = n + kUnitCost;
+            auto block_at = [&](int64_t y) { return static_cast<int>(min(max(y - kUnitCost / 2, int64_t(0)), static_cast<int64_t>(n))); };
             for (int head = 0; head < a.c.H_kv; ++head) {
-                const int64_t x0 = before * a.c.H_kv + static_cast<int64_t>(head) * n, x1 = x0 + n;
+                const int64_t x0 = before * a.c.H_kv + static_cast<int64_t>(head) * w, x1 = x0 + w;
                 const int j = i * a.c.H_kv + head;
-                const int c0 = static_cast<int>(min(x0 / share, static_cast<int64_t>(t.grid - 1)));
-                const int c1 = n > 0 ? static_cast<int>((x1 - 1) / share) : c0;
+                int c0 = static_cast<int>(x0 / share), c1 = n > 0 ? static_cast<int>((x1 - 1) / share) : c0;
+                bool at_start = x0 == c0 * share;  // of c0's share
+                if (n > 0 && block_at((c0 + 1) * share - x0) == 0) {  // nothing but the front
+                    ++c0;
+                    at_start = true;
+                }
+                if (c1 > c0 && block_at(c1 * share - x0) == n) --c1;  // nothing but what is behind
                 u.head = head;
-                const int slot0 = 2 * c0 + (x0 == c0 * share ? 0 : 1);
+                const int slot0 = 2 * c0 + (at_start ? 0 : 1);
                 for (int c = c0; c <= c1; ++c) {
-                    const int64_t y0 = max(x0, c * share), y1 = min(x1, (c + 1) * share);
-                    u.vb0 = static_cast<int>(y0 - x0);
-                    u.nblk = n > 0 ? static_cast<int>(y1 - y0) : 0;
+                    u.vb0 = block_at(c == c0 ? 0 : c * share - x0);
+                    u.nblk = block_at(c == c1 ? w : (c + 1) * share - x0) - u.vb0;
                     u.slot = c1 == c0 ? -1 : c == c0 ? slot0 : 2 * c;
                     t.units[j + c] = u;
                     atomicMin(&s_first[c], j + c);
@@ -277,7 +286,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(TcArgs t) {
                 }
                 if (c1 > c0) t.joins[atomicAdd(&s_joins, 1)] = TcJoin{u.token0, u.ntok, head, slot0, c0, c1 - c0 + 1};
             }
-            before += n;
+            before += w;
         }
         __syncthreads();
         if (tid < t.grid) t.ranges[tid] = make_int2(s_first[tid], s_last[tid] < 0 ? 0 : s_last[tid] - s_first[tid] + 1);
