@@ -1,0 +1,80 @@
+"""Two host threads that call at the same time, each on its own stream and with
+its own workspace and output.  ctypes releases the interpreter's lock in a call,
+so their launches interleave; neither may change what the other's launch is
+allowed to take, nor its result."""
+import threading
+
+import pytest
+import torch
+
+import w8a8_activation_quantized_b200 as cider
+from tests.paged_cases import Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def _at_once(calls, times):
+    """Runs each of `calls` `times` times in a thread of its own, all started
+    together; the first exception of any of them is raised."""
+    start, errors = threading.Barrier(len(calls)), []
+
+    def work(call):
+        start.wait()
+        try:
+            for _ in range(times):
+                call()
+                if errors:
+                    return
+        except Exception as e:  # noqa: BLE001 (raised below, in the test's thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    if errors:
+        raise errors[0]
+
+
+@pytest.mark.parametrize("what", ["paged 16-row tiles", "paged tensor-core tiles", "decode attention", "per-channel product"])
+def test_a_thread_whose_first_use_of_cuda_is_the_call(what):
+    """Everything is allocated beforehand, so the thread makes no other call first."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    stream = torch.cuda.Stream()
+    if what.startswith("paged"):
+        cider.cider_test_set_paged_kernel(1 if "16" in what else 2)
+        b = Batch([(300, 40), (40, 1)], 8, 2, D=64, page=32, seed=3)
+        ws = torch.empty(cider.cider_paged_attention_workspace_bytes(b.T, 2, 8, 2, 64, 40), dtype=torch.uint8, device="cuda")
+
+        def call(out, st):
+            return b.run(cider, out=out, workspace=ws, stream=st)
+        like = b.q
+    elif what == "decode attention":
+        q, k, v = (torch.randn(s, generator=g, device="cuda").half() for s in ((8, 128), (2, 500, 128), (2, 500, 128)))
+        ws = torch.empty(cider.cider_sdpa_decode_workspace_bytes(8, 2, 500, 128), dtype=torch.uint8, device="cuda")
+
+        def call(out, st):
+            return cider.cider_sdpa_decode(q, k, v, out=out, workspace=ws, stream=st)
+        like = q
+    else:
+        x, w = (torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8) for s in ((200, 256), (264, 256)))
+        sx, sw = (torch.rand(n, generator=g, device="cuda") for n in (200, 264))
+
+        def call(out, st):
+            return cider.cider_w8a8_gemm_pc_q(x, sx, w, sw, y=out, stream=st)
+        like = torch.empty((200, 264), dtype=torch.float16, device="cuda")
+    try:
+        want, out = call(torch.zeros_like(like), stream), torch.zeros_like(like)
+        torch.cuda.synchronize()
+        _at_once([lambda: call(out, stream)], 1)
+        assert torch.equal(out, want)
+    finally:
+        cider.cider_test_set_paged_kernel(0)
