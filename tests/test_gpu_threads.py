@@ -78,3 +78,41 @@ def test_a_thread_whose_first_use_of_cuda_is_the_call(what):
         assert torch.equal(out, want)
     finally:
         cider.cider_test_set_paged_kernel(0)
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+def test_paged_attention_of_small_and_large_batches(kernel, monkeypatch):
+    """The kernels' shared memory grows with the number of requests.  The calls
+    go to the library as the binding makes them, but back to back, so that they
+    meet often."""
+    cider.cider_test_set_paged_kernel(kernel)
+    try:
+        large = [(i % 40, 1) if i % 512 == 511 else (0, 0) for i in range(4096)]
+        bs = [Batch(lens, 8, 2, D=64, page=32, seed=i) for i, lens in enumerate(([(40, 1)], large, [(17, 1)], large))]
+        want = [b.run(cider) for b in bs]
+        outs = [torch.zeros_like(w) for w in want]
+        ws = [torch.empty(cider.cider_paged_attention_workspace_bytes(b.T, len(b.lens), 8, 2, 64, 1), dtype=torch.uint8,
+                          device="cuda") for b in bs]
+        streams = [torch.cuda.Stream() for _ in bs]
+        made = []
+        monkeypatch.setattr(cider, "_paged_call", lambda name, index, stream, *args: made.append((name, args, stream)))
+        for b, o, w, s in zip(bs, outs, ws, streams):
+            b.run(cider, out=o, workspace=w, stream=s)
+        monkeypatch.undo()
+        torch.cuda.synchronize()
+
+        def calls(name, args, stream):
+            f, st = getattr(cider.lib(), name), stream.cuda_stream
+
+            def some():
+                for _ in range(100):
+                    status = f(*args, st)
+                    if status != 0:
+                        cider._check(name, status)
+                stream.synchronize()
+            return some
+        _at_once([calls(*m) for m in made], 100)
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        cider.cider_device_status()
+    finally:
+        cider.cider_test_set_paged_kernel(0)

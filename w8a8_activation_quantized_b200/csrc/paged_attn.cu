@@ -733,7 +733,9 @@ cudaError_t launch_t(PagedAttnArgs a, int num_sms, cudaStream_t st) {
     const int ring = 1024 + kRing<D> * 2 * kBlock * D * 2;
     const int pre = (a.B + 1) * 8;
     auto kern = k_paged_attn<T, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + pre);
+    // The limit is the function's, for all host threads: the most that any call
+    // takes, since one call's own size could be in force at another's launch.
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + (kPagedMaxRequests + 1) * 8);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(a.grid), dim3(kThreads), ring + pre, st, tmK, tmV, a);
     if (e != cudaSuccess) return e;

@@ -1191,7 +1191,9 @@ cudaError_t launch_tc(const PagedAttnArgs& p, int num_sms, cudaStream_t st) {
     auto kern = k_paged_tc<T, D>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     const int plan_smem = (4 * p.B + 1) * 4;
-    if ((e = cudaFuncSetAttribute(k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_smem)) != cudaSuccess) return e;
+    // the most that any call takes: the limit is the function's, for all host threads
+    e = cudaFuncSetAttribute(k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (4 * kPagedMaxRequests + 1) * 4);
+    if (e != cudaSuccess) return e;
     if ((e = launch_pdl(k_paged_plan, dim3(1), dim3(kPlanThreads), plan_smem, st, t)) != cudaSuccess) return e;
     if ((e = launch_pdl(kern, dim3(t.grid), dim3(kTcThreads), smem, st, tmQ, tmK, tmV, t)) != cudaSuccess) return e;
     // as many CTAs as are resident: a row is a few dependent loads
