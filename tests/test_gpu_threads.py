@@ -116,3 +116,40 @@ def test_paged_attention_of_small_and_large_batches(kernel, monkeypatch):
         cider.cider_device_status()
     finally:
         cider.cider_test_set_paged_kernel(0)
+
+
+@pytest.mark.parametrize("product", ["w8a8", "w8a16"])
+@pytest.mark.parametrize("kernel", [1, 2, 3, 4])
+def test_decode_products_of_few_and_more_rows(kernel, product):
+    """The decode kernels' shared memory grows with the rows.  Calls back to
+    back, straight to the library."""
+    cider.cider_test_set_small_m_kernel(kernel)
+    try:
+        g = torch.Generator(device="cuda").manual_seed(7)
+        N, K = 520, 10240
+        w = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+        sw = torch.rand(N, generator=g, device="cuda")
+        xs = [torch.randn((M, K), generator=g, device="cuda").half() for M in (2, 4, 2, 4)]
+        f = getattr(cider.lib(), "cider_w8a8_linear_pc" if product == "w8a8" else "cider_w8a16_mv_pc")
+        call = cider.cider_w8a8_linear_pc if product == "w8a8" else cider.cider_w8a16_mv_pc
+        want = [call(x, w, sw) for x in xs]
+        ys = [torch.zeros_like(y) for y in want]
+        streams = [torch.cuda.Stream() for _ in xs]
+        torch.cuda.synchronize()
+
+        def calls(x, y, stream):
+            a = [x.data_ptr(), cider._DT[x.dtype], x.shape[0], K, w.data_ptr(), sw.data_ptr(), N, y.data_ptr(),
+                 cider._DT[y.dtype]] + ([None, 0] if product == "w8a8" else []) + [stream.cuda_stream]
+
+            def some():
+                for _ in range(100):
+                    status = f(*a)
+                    if status != 0:
+                        cider._check(f.__name__, status)
+                stream.synchronize()
+            return some
+        _at_once([calls(*m) for m in zip(xs, ys, streams)], 100)
+        assert all(torch.equal(y, v) for y, v in zip(ys, want))
+        cider.cider_device_status()
+    finally:
+        cider.cider_test_set_small_m_kernel(0)

@@ -27,10 +27,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxK = 131072;            // 127 * 128 * K < 2^31 keeps INT32 exact
 constexpr int64_t kMaxSmallM = 16;
-constexpr int64_t kSmallSmemLimit = 160 * 1024;  // q rows of the small-M kernel in shared memory
 constexpr int64_t kSmallMaxK = 32768;
 constexpr int kMaxMvM = 4;                        // rows of the W8A16 decode kernel
-constexpr int kMaxSmallXBytes = 160 * 1024;       // its fp32 activation rows in shared memory
 
 struct DeviceInfo {
     int ready = 0;     // 1 = filled in
@@ -112,7 +110,7 @@ size_t tensor_path_bytes(int64_t M, int64_t K) {
 }
 
 bool small_m_path(int64_t M, int64_t K) {
-    return M >= 1 && M <= g_small_m_threshold.load() && M * K <= kSmallSmemLimit && K <= kSmallMaxK;
+    return M >= 1 && M <= g_small_m_threshold.load() && M * K <= kSmallRowsBytes && K <= kSmallMaxK;
 }
 
 // Common checks of the linear / GEMM entry points.
@@ -517,9 +515,9 @@ cider_status_t cider_w8a16_mv_pc(const void* x, cider_dtype_t xdt, int64_t M, in
     if (M == 0) return CIDER_OK;
     if (M > kMaxMvM) return fail(CIDER_ERR_INVALID_ARG, "M = %lld exceeds %d (decode shapes only)", (long long)M, kMaxMvM);
     const int64_t xbytes = M * ((K / 16 + 31) / 32) * 2048;  // fp32 activations, whole 512-wide passes
-    if (xbytes > kMaxSmallXBytes)
+    if (xbytes > kSmallRowsBytes)
         return fail(CIDER_ERR_INVALID_ARG, "%lld bytes of staged activations exceed %d", (long long)xbytes,
-                    kMaxSmallXBytes);
+                    kSmallRowsBytes);
     if (K > kSmallMaxK) return fail(CIDER_ERR_INVALID_ARG, "K = %lld exceeds %lld", (long long)K, (long long)kSmallMaxK);
     const Range ry = rng(y, static_cast<size_t>(M) * N * 2);
     if (overlap(ry, rng(x, static_cast<size_t>(M) * K * 2)) || overlap(ry, rng(w, static_cast<size_t>(N) * K)) ||
@@ -542,9 +540,9 @@ cider_status_t cider_w8a16_mv_pg(const void* x, cider_dtype_t xdt, int64_t M, in
     if (M == 0) return CIDER_OK;
     if (M > kMaxMvM) return fail(CIDER_ERR_INVALID_ARG, "M = %lld exceeds %d (decode shapes only)", (long long)M, kMaxMvM);
     const int64_t xbytes = M * ((K / 16 + 31) / 32) * 2048;  // fp32 activations, whole 512-wide passes
-    if (xbytes > kMaxSmallXBytes)
+    if (xbytes > kSmallRowsBytes)
         return fail(CIDER_ERR_INVALID_ARG, "%lld bytes of staged activations exceed %d (shared memory)",
-                    (long long)xbytes, kMaxSmallXBytes);
+                    (long long)xbytes, kSmallRowsBytes);
     if (K > kSmallMaxK) return fail(CIDER_ERR_INVALID_ARG, "K = %lld exceeds %lld", (long long)K, (long long)kSmallMaxK);
     const Range ry = rng(y, static_cast<size_t>(M) * N * 2);
     if (overlap(ry, rng(x, static_cast<size_t>(M) * K * 2)) || overlap(ry, rng(w, static_cast<size_t>(N) * K)) ||

@@ -14,6 +14,10 @@ namespace cider {
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusIndex = 2u;  // a length, page number or slot in device memory outside its range
 
+// Most bytes of activation rows that a decode kernel keeps in shared memory
+// (codes, or the fp32 values of the W8A16 products).
+constexpr int kSmallRowsBytes = 160 * 1024;
+
 enum : int {
     kModePC = 0,    // per-channel dequant epilogue
     kModePG = 1,    // per-group dequant epilogue

@@ -1152,9 +1152,11 @@ static cudaError_t launch_small_t(const void* x, int M, int K, const void* w, co
                                   void* y, int ydt, const SmallGeom& geo, int num_sms, cudaStream_t st) {
     const size_t smem = static_cast<size_t>(M) * K;
     auto kern = k_small_m<TX, PG, W4, MAXM, PPW>;
-    // opt in above the default 48 KB: static shared memory counts against it too
+    // opt in above the default 48 KB: static shared memory counts against it too;
+    // here and below to the most that any call takes, because the limit is the
+    // function's, for all host threads
     if (smem > 32 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallRowsBytes);
         if (e != cudaSuccess) return e;
     }
     const int grid = geo.nblocks < 2 * num_sms ? geo.nblocks : 2 * num_sms;
@@ -1232,7 +1234,7 @@ template <typename TX, bool PG, bool W4, int MAXM, int PPL>
 static cudaError_t launch_bulk_t(const void* x, int M, int K, const void* w, const float* sw, int N, int gs, void* y,
                                  int ydt, const BulkGeom& geo, int grid, unsigned* status, cudaStream_t st) {
     auto kern = k_small_m_bulk<TX, PG, W4, MAXM, PPL>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, geo.smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkSmemBytes);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, grid, kBulkThreads, geo.smem, st, static_cast<const TX*>(x), M, K,
                       static_cast<const uint8_t*>(w), sw, N, gs, y, ydt, geo, status);
@@ -1286,7 +1288,7 @@ static cudaError_t launch_shot_t(const void* x, int M, int K, const void* w, con
                                  cudaStream_t st) {
     auto kern = k_small_m_shot<TX, PG, W4, MAXM, A16>;
     if (smem > 32 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kShotSmemBytes);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(kern, grid, kShotThreads, smem, st, static_cast<const TX*>(x), M, K,
@@ -1337,7 +1339,7 @@ static cudaError_t launch_mv_t(const void* x, int M, int K, const int8_t* w, con
     auto kern = k_mv_w8a16<TX, PG, MAXM, PPW>;
     // opt in above the default 48 KB: static shared memory counts against it too
     if (smem > 32 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallRowsBytes);
         if (e != cudaSuccess) return e;
     }
     const int grid = geo.nblocks < 2 * num_sms ? geo.nblocks : 2 * num_sms;
@@ -1367,7 +1369,7 @@ static cudaError_t launch_mv_bulk_t(const void* x, int M, int K, const int8_t* w
                                     void* y, int ydt, const BulkGeom& geo, int grid, unsigned* status,
                                     cudaStream_t st) {
     auto kern = k_mv_w8a16_bulk<TX, PG, MAXM, PPL>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, geo.smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkSmemBytes);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, grid, kBulkThreads, geo.smem, st, static_cast<const TX*>(x), M, K, w, sw, N, gs, y, ydt,
                       geo, status);
