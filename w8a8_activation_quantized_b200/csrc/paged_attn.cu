@@ -445,9 +445,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[j][e] += sa[j][e];
                 // Masks, unless every row sees every key of the step.  A row that has
-                // seen a key has a finite maximum, even if the score was -inf (its
-                // result is then 0 / 0, as the formula's), and only one that has seen
-                // none keeps -inf (its result is 0).
+                // seen a key has a finite maximum, even if its scores were all -inf
+                // (-FLT_MAX, a mark; if that stays its result is 0 / 0, as the
+                // formula's), and only one that has seen none keeps -inf (its result is 0).
                 float low[2] = {-FLT_MAX, -FLT_MAX};
                 const bool whole = !lost && key0 + kStep - 1 <= span.pmin &&
                                    (a.window <= 0 || key0 > span.pmax - a.window || key0 + kStep <= a.sinks);
@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
                 float p[2][4];
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    const float ms = (m[hh] == -INFINITY ? 0.0f : m[hh]) * a.qscale - kPOff<T>;  // nothing seen yet: all p = 0
+                    // no score above -inf yet: all p = 0 (the mark times the scale may overflow)
+                    const float ms = (m[hh] <= -FLT_MAX ? 0.0f : m[hh]) * a.qscale - kPOff<T>;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll

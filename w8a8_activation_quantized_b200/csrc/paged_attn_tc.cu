@@ -478,7 +478,7 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int row) {
                 for (int w = 16; w > 0; w >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], w);
                 if (paged_sees(key0 + i, pos, a.window, a.sinks)) mn = fmaxf(fmaxf(mn, s[i]), -FLT_MAX);
             }
-            const float f = mn == m ? 1.0f : ex2((m - mn) * a.qscale), ms = kOff<T> - mn * a.qscale;
+            const float f = mn == m ? 1.0f : ex2((m - mn) * a.qscale), ms = kOff<T> - (mn <= -FLT_MAX ? 0.0f : mn) * a.qscale;
             m = mn;
             l *= f;
 #pragma unroll
@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     if (!kApart<D> && i > 0) mbar_arrive(&vempty[(gb + i - 1) % VS]);
                     if (i + 1 == u.nblk) mbar_arrive(&qempty);
                 }
-                float low = -FLT_MAX;  // a row that has seen a key has a finite maximum
+                float low = -FLT_MAX;  // a row that has seen a key has a finite maximum: this mark, if its scores were all -inf
                 const uint32_t lost = s_lost[(gb + i) & 7];
                 const bool whole = !lost && key0 + kKeys - 1 <= pmin &&
                                    (a.window <= 0 || key0 > pmax - a.window || key0 + kKeys <= a.sinks);
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 const float mx = max3_nan(max3_nan(mc[0], mc[1], mc[2]), mc[3], mc[3]);
                 // From -inf it always moves.  A NaN score makes the row NaN, and so
                 // does +inf (inf - inf), as in the formula.
-                const bool grow = m != mx && !((mx - m) * a.qscale <= kLazy);
+                const bool grow = !(mx <= m) && (m <= -FLT_MAX || !((mx - m) * a.qscale <= kLazy));
                 float f = 1.0f;
                 if (grow) {
                     f = ex2((m - mx) * a.qscale);
@@ -950,7 +950,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     }
                     tmem_st_wait();
                 }
-                const float ms = kOff<T> - (m == -INFINITY ? 0.0f : m) * a.qscale;  // nothing seen yet: all weights 0
+                // no score above -inf yet: all weights 0 (the mark times the scale may overflow)
+                const float ms = kOff<T> - (m <= -FLT_MAX ? 0.0f : m) * a.qscale;
                 const uint64_t qs2 = pack_f32x2(a.qscale, a.qscale), ms2 = pack_f32x2(ms, ms);
                 uint64_t l2[4] = {0, 0, 0, 0};
                 // 64 keys' weights, from the scores in x[0] and x[1]
