@@ -406,7 +406,8 @@ CIDER_API cider_status_t cider_paged_append(const cider_paged_cache_t* cache, co
  * workspace: cider_paged_attention_workspace_bytes(...) bytes, 16-byte aligned;
  * calls that may run at the same time need one each.
  * A value in V that is not finite costs time: in the chunks' kernel the rows of
- * its block of queries are computed again key by key (up to 2 us per key).
+ * its block of queries are computed again key by key (up to 2 us per key).  So
+ * does a query whose largest |scale * log2(e) * (q . K)| is 2^16 or more.
  * In device memory, reported by cider_device_status(): cu_fresh outside [0, T]
  * is cut to it; where it decreases, the request has no tokens, and rows that
  * several requests then claim are not defined; kv_len outside [0, width *

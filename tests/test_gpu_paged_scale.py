@@ -73,3 +73,42 @@ def test_keys_of_score_minus_infinity_have_no_weight(kernel, lens, keys, scale, 
     smax = b.oracle()[2]  # of the finite products
     check(b, out, (want, np.where(np.isfinite(mag), mag, 0), smax, cnt))
     assert (~nan[cnt > 0]).any()
+
+
+@pytest.mark.parametrize("lens,window", [([(1, 1), (700, 1)], 0), ([(9000, 1)], 0), ([(300, 5), (129, 3)], 0),
+                                         ([(260, 129), (33, 33)], 0), ([(5000, 40)], 0), ([(900, 200)], 100)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dt,power", [("f16", 0), ("f16", 4), ("f16", 8), ("f16", 15), ("bf16", 0), ("bf16", 16), ("bf16", 60),
+                                      ("bf16", 110)])
+def test_large_scores(kernel, dt, power, sign, D, lens, window):
+    """All dims of a query are 2^power and all dims of a key one small integer,
+    so scores are exact in fp32 and differ by D 2^power at least: a query's
+    weight is shared evenly by the seen keys of the largest integer, however
+    large the scores are.
+
+    Off by: the weights of those keys 4 e each (ex2.approx; the same for all) and
+    e per rescale or join (R = N / 16 + 8), twice; their sums 2 N e, twice; P once
+    u; the division and its product 3 e; the result u, in fp16 half of the smallest
+    subnormal.  Where the scores lie below 2^16 in base two, the product of the
+    maximum and the scale is off by 2^-9 at most: 2^-9 ln 2 per weight, twice.  The
+    others' weights are below 2^-60 (D 2^power scale log2 e >= 64 x 1.44)."""
+    b = Batch(lens, 8, 2, D=D, page=32, dt=dt, seed=D + power + len(lens), window=window)
+    t = b.q.dtype
+    g = torch.Generator(device="cuda").manual_seed(power)
+    b.q = torch.full_like(b.q, 2.0 ** power)
+    own = ~b.k.isnan()
+    lo, hi = (1000, 1008) if dt == "f16" else (200, 208)
+    k = torch.randint(lo, hi, b.k.shape[:3] + (1,), generator=g, device="cuda") * sign
+    b.k = torch.where(own, k.to(t), b.k)
+    if dt == "bf16" and power == 110:  # D 2^110 200 stays below 2^127
+        b.k = b.k / 4
+    b.scale = 1.0
+    got = b.run(cider, scale=1.0).double().cpu().numpy()
+    want, mag, _, cnt = b.oracle()
+    u, e = (2.0 ** -11, 2.0 ** -24) if dt == "f16" else (2.0 ** -8, 2.0 ** -24)
+    n = cnt[:, None, None]
+    rel = u + 2 * (4 * e + (n / 16 + 8) * 5 * e + 2 * n * e) + 3 * e + 2 * 2.0 ** -9 * np.log(2)
+    tol = rel * mag * (1 + u) + u * np.abs(want) + (2.0 ** -25 if dt == "f16" else 0.0)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), f"{(~(err <= tol)).sum()} of {err.size} off, worst {np.nanmax(err / tol)} of the tolerance"

@@ -508,13 +508,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
                 float p[2][4];
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    // no score above -inf yet: all p = 0 (the mark times the scale may overflow)
-                    const float ms = (m[hh] <= -FLT_MAX ? 0.0f : m[hh]) * a.qscale - kPOff<T>;
+                    // The difference comes before the scale: m times the scale would be rounded
+                    // to more than a unit of the exponent for large scores, and may overflow.
+                    const float mu = m[hh] == -INFINITY ? 0.0f : m[hh];  // nothing seen yet: all p = 0
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            p[j][2 * hh + e] = ex2(fmaf(sc[j][2 * hh + e], a.qscale, -ms));
+                            p[j][2 * hh + e] = ex2(fmaf(sc[j][2 * hh + e] - mu, a.qscale, kPOff<T>));
                             l[hh] += p[j][2 * hh + e];
                         }
                 }

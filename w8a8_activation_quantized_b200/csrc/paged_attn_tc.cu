@@ -29,7 +29,8 @@
 //    weights.  Other rows of V are tokens' values: finite, as a rule.  If one that
 //    some query does not see is not, 0 x V makes that query's output NaN; a row
 //    whose output is not finite although its weights' sum is gets computed again
-//    by its warp (redo_row), from the keys that it sees alone.
+//    by its warp (redo_row), from the keys that it sees alone.  So is a row with scores
+//    of 2^16 or more (scaled, in base two).
 //
 // What bounds it: per 128 x 128 block of scores the two products take 1024
 // cycles of the tensor pipe at D = 128 (8192 fp16 operations per cycle and SM),
@@ -71,6 +72,10 @@ constexpr int kMaxCut = 2560;                  // units up to which they may be 
 constexpr int kUnitCost = 2;                   // the start and end of a unit, in blocks
 constexpr int kMinShare = 2 + kUnitCost;       // length per CTA where the line is cut
 constexpr float kLazy = 8.0f;                  // log2 of the growth of a maximum that is put off
+// The exponents are s q - m q (q the scale, in base two), one operation per score; below this
+// |m q| the rounding of m q, which is the same for all keys until m moves, is 2^-9 at
+// most.  Rows beyond it are computed again with (s - m) q.
+constexpr float kFar = 65536.0f;
 
 // One unit: tokens [token0, token0 + ntok) of q's rows, the first at position
 // pmin, against blocks [vb0, vb0 + nblk) of its span; slot -1: the whole span.
@@ -478,7 +483,7 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int row) {
                 for (int w = 16; w > 0; w >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], w);
                 if (paged_sees(key0 + i, pos, a.window, a.sinks)) mn = fmaxf(fmaxf(mn, s[i]), -FLT_MAX);
             }
-            const float f = mn == m ? 1.0f : ex2((m - mn) * a.qscale), ms = kOff<T> - (mn <= -FLT_MAX ? 0.0f : mn) * a.qscale;
+            const float f = mn == m ? 1.0f : ex2((m - mn) * a.qscale);
             m = mn;
             l *= f;
 #pragma unroll
@@ -486,7 +491,7 @@ __device__ __noinline__ void redo_row(const TcArgs& t, TcUnit u, int row) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (!paged_sees(key0 + i, pos, a.window, a.sinks)) continue;
-                const float p = ex2(fmaf(s[i], a.qscale, ms));
+                const float p = ex2(fmaf(s[i] - mn, a.qscale, kOff<T>));
                 l += p;
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[e] = fmaf(p, to_f32<T>(reinterpret_cast<const T*>(&v[i])[e]), o[e]);
@@ -1055,8 +1060,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 }
             }
             // NaN or an infinity in O although the weights' sum is finite: it came from V,
-            // perhaps from a row of it that this query does not see.
-            for (uint32_t rows = __ballot_sync(0xffffffffu, odd && live && l < INFINITY); rows; rows &= rows - 1) {
+            // perhaps from a row of it that this query does not see.  Or scores too large for
+            // the product of the maximum and the scale (m is neither NaN nor a mark).
+            odd = odd && l < INFINITY;
+            odd |= m > -FLT_MAX && fabsf(m * a.qscale) >= kFar;
+            for (uint32_t rows = __ballot_sync(0xffffffffu, odd && live); rows; rows &= rows - 1) {
                 __syncwarp();  // its lane's stores are overwritten
                 redo_row<T, D>(t, u, h * 128 + (warp & 3) * 32 + __ffs(rows) - 1);
             }
