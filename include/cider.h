@@ -87,12 +87,14 @@ CIDER_API const char* cider_status_string(cider_status_t status);
  * string stays valid until the next call on the same thread. */
 CIDER_API const char* cider_last_error(void);
 
-/* Synchronises `stream`, then reads and clears the device status word of the
- * current device: CIDER_OK, or CIDER_ERR_TIMEOUT if a bounded wait in some
- * kernel ran out since the last read, or CIDER_ERR_INVALID_ARG if a paged-cache
- * kernel met a length, page number or slot in device memory that its call does
- * not allow (each entry point says what it does with such a value; none of
- * them reads or writes outside the caller's buffers).  Not for the hot path. */
+/* Synchronises `stream`, then reads the device status word of the current
+ * device: CIDER_OK, or CIDER_ERR_TIMEOUT if a bounded wait in some kernel ran
+ * out, or CIDER_ERR_INVALID_ARG if a paged-cache kernel met a length, page
+ * number or slot in device memory that its call does not allow (each entry
+ * point says what it does with such a value; none of them reads or writes
+ * outside the caller's buffers).  What it returns is cleared; where both have
+ * happened, the timeout comes first and the next call returns the other.  Not
+ * for the hot path. */
 CIDER_API cider_status_t cider_device_status(void* stream);
 
 /* Bytes of workspace the linear entry points need for M tokens of K inputs:

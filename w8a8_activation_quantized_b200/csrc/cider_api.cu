@@ -24,6 +24,8 @@ __device__ unsigned g_status_word;
 
 namespace {
 
+__global__ void k_clear_status(unsigned* word, unsigned bits) { atomicAnd(word, ~bits); }
+
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxK = 131072;            // 127 * 128 * K < 2^31 keeps INT32 exact
 constexpr int64_t kMaxSmallM = 16;
@@ -423,11 +425,14 @@ cider_status_t cider_device_status(void* stream) {
     if ((e = cudaMemcpy(&v, d->status, sizeof v, cudaMemcpyDeviceToHost)) != cudaSuccess)
         return cuda_fail(e, "reading the status word");
     if (v != 0) {
-        unsigned zero = 0;
-        if ((e = cudaMemcpy(d->status, &zero, sizeof zero, cudaMemcpyHostToDevice)) != cudaSuccess)
+        // only the bit that this call reports, and as an atomic: the other one, and
+        // what kernels on other streams add meanwhile, stay for the next read
+        const unsigned bit = v & kStatusTimeout ? kStatusTimeout : v & kStatusIndex ? kStatusIndex : v;
+        k_clear_status<<<1, 1, 0, st>>>(d->status, bit);
+        if ((e = cudaGetLastError()) != cudaSuccess || (e = cudaStreamSynchronize(st)) != cudaSuccess)
             return cuda_fail(e, "clearing the status word");
-        if (v & kStatusTimeout) return fail(CIDER_ERR_TIMEOUT, "a bounded device-side wait ran out");
-        if (v & kStatusIndex)
+        if (bit == kStatusTimeout) return fail(CIDER_ERR_TIMEOUT, "a bounded device-side wait ran out");
+        if (bit == kStatusIndex)
             return fail(CIDER_ERR_INVALID_ARG,
                         "a paged-cache call met a length, page number or slot in device memory outside its range");
     }
