@@ -88,10 +88,14 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Barrier of the warps that compute.
-__device__ __forceinline__ void users_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kUsers) : "memory"); }
+__device__ __forceinline__ void users_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(kUsers) : "memory");
+}
 
 __device__ __forceinline__ bool users_or(bool x) {  // true if any thread passes true
     uint32_t y;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"

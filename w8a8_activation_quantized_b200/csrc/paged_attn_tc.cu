@@ -408,6 +408,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // Barrier of the 128 threads of softmax warpgroup wg; true if any passes x.
 __device__ __forceinline__ bool group_or(int wg, bool x) {
     uint32_t y;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
@@ -843,6 +844,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     if (!kApart<D> && i > 0) mbar_arrive(&vempty[(gb + i - 1) % VS]);
                     if (i + 1 == u.nblk) mbar_arrive(&qempty);
                 }
+                __syncwarp();  // the loads from tensor memory are the whole warp's; so below, behind one lane's arrivals
                 float low = -FLT_MAX;  // a row that has seen a key has a finite maximum: this mark, if its scores were all -inf
                 const uint32_t lost = s_lost[(gb + i) & 7];
                 const bool whole = !lost && key0 + kKeys - 1 <= pmin &&
@@ -932,12 +934,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 // From -inf it always moves.  A NaN score makes the row NaN, and so
                 // does +inf (inf - inf), as in the formula.
                 const bool grow = !(mx <= m) && (m <= -FLT_MAX || !((mx - m) * a.qscale <= kLazy));
-                float f = 1.0f;
-                if (grow) {
-                    f = ex2((m - mx) * a.qscale);
-                    m = mx == INFINITY ? NAN : mx;
-                    l *= f;
-                }
+                const float f = grow ? ex2((m - mx) * a.qscale) : 1.0f;
+                m = !grow ? m : mx == INFINITY ? NAN : mx;
+                l *= f;
                 if (kApart<D> && i > 0) {  // the last block's product is done: with P, and O is complete
                     if (ok) ok = tile_wait(&odone[h][(nb - 1) & 1], ((nb - 1) >> 1) & 1, status, abort_flag);
                     __syncwarp();
@@ -978,9 +977,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     }
                     weights(sr, p[0]);
                     weights(sr + 2, p[1]);
-                    if (paired && lane == 0 && !(h == 1 && i + 1 == u.nblk)) mbar_arrive(other_turn);
                     tmem_st_32x32b_x32(tP, p[0]);
                     tmem_st_32x32b_x32(tP + 32, p[1]);
+                    if (paired && lane == 0 && !(h == 1 && i + 1 == u.nblk)) mbar_arrive(other_turn);
+                    __syncwarp();
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -998,6 +998,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&pfull[h][0]);  // 64 keys' weights: their half of the product may start
+                    __syncwarp();
                     ld_wait(sr[0]);
                     ld_wait(sr[1]);
                     weights(sr, p);
@@ -1030,6 +1031,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
+                __syncwarp();  // rows that are not live leave the loop's body early
                 if (u.nblk > 0) {
                     tmem_ld_32x32b_x32(tO + c * 32, o);
                     ld_wait(o);
