@@ -428,9 +428,9 @@ cider_status_t cider_device_status(void* stream) {
         // only the bit that this call reports, and as an atomic: the other one, and
         // what kernels on other streams add meanwhile, stay for the next read
         const unsigned bit = v & kStatusTimeout ? kStatusTimeout : v & kStatusIndex ? kStatusIndex : v;
-        k_clear_status<<<1, 1, 0, st>>>(d->status, bit);
-        if ((e = cudaGetLastError()) != cudaSuccess || (e = cudaStreamSynchronize(st)) != cudaSuccess)
-            return cuda_fail(e, "clearing the status word");
+        void* args[] = {&d->status, const_cast<unsigned*>(&bit)};
+        e = cudaLaunchKernel(reinterpret_cast<const void*>(&k_clear_status), dim3(1), dim3(1), args, 0, st);
+        if (e != cudaSuccess || (e = cudaStreamSynchronize(st)) != cudaSuccess) return cuda_fail(e, "clearing the status word");
         if (bit == kStatusTimeout) return fail(CIDER_ERR_TIMEOUT, "a bounded device-side wait ran out");
         if (bit == kStatusIndex)
             return fail(CIDER_ERR_INVALID_ARG,
