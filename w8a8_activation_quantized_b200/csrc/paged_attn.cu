@@ -639,9 +639,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
 // Joins the pieces of the tile in CTA c's record, c = blockIdx.x:
 // out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M), kJoinPieces at a time.  A
 // tile may have as many pieces as there are CTAs, so the threads that a tile's
-// rows leave over share the pieces.  A CTA is small enough (registers, shared
-// memory) to be resident beside two of the kernel before it, and waits there: 8.4
-// us by itself, about 4 behind that kernel.
+// rows leave over share the pieces.  Beside two CTAs of the kernel before it (168
+// registers for each of 160 threads; D = 64: 158) an SM has no room for one of these
+// (48 registers for each of 256); it enters when one of the two has left and waits
+// for the others: 8.4 us by itself, about 4 behind that kernel.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinPieces = 32;
 constexpr int kJoinSplit = 4;  // CTAs per record, each for a quarter of the dims
