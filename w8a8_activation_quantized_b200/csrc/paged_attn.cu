@@ -523,7 +523,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_paged_attn(const __gri
                             l[hh] += p[j][2 * hh + e];
                         }
                 }
-                // O += P V
+                // O += P V.  P is rounded to the 16-bit type, the operand's of the product:
+                // off by half a unit per weight, as the result is once more.  (A second part
+                // for the rest would double these products; against 64 bits the error is 2 to 11 %
+                // above that of weights in fp32.)  l sums the weights before the rounding.
                 if (!slow) {
                     uint32_t pa[4];
                     pa[0] = pack2_out<T>(p[0][0], p[0][1]);

@@ -958,7 +958,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_tc(const __grid_constan
                 const float ms = kOff<T> - (m <= -FLT_MAX ? 0.0f : m) * a.qscale;
                 const uint64_t qs2 = pack_f32x2(a.qscale, a.qscale), ms2 = pack_f32x2(ms, ms);
                 uint64_t l2[4] = {0, 0, 0, 0};
-                // 64 keys' weights, from the scores in x[0] and x[1]
+                // 64 keys' weights, from the scores in x[0] and x[1].  They are rounded to the
+                // 16-bit type, the operand's of the product with V: off by half a unit each, as
+                // the result is once more.  (A second part for the rest would double that product
+                // and P's room; against 64 bits the error is 28 to 40 % above that of weights in
+                // fp32.)  l sums them before the rounding.
                 auto weights = [&](const uint32_t (*x)[32], uint32_t (&p)[32]) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
