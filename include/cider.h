@@ -37,8 +37,8 @@
  *    gs is 64 or 128 and divides K; W4A8 also needs K % 32 == 0; y must not
  *    overlap any input or the workspace (checked by address range).
  *  - Calls may come from several host threads at the same time, each with
- *    outputs and a workspace of its own; the test switches at the end of this
- *    file are process-wide.
+ *    outputs and a workspace of its own (the workspace-free entry point has
+ *    one scratch for all); the test switches are process-wide.
  *  - On a device that is not compute capability 10.x the calls return
  *    CIDER_ERR_UNSUPPORTED; there is no CPU fallback.
  *  - Launch failures return CIDER_ERR_CUDA.  Faults that happen later on the
