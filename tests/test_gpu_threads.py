@@ -72,7 +72,9 @@ def test_a_thread_whose_first_use_of_cuda_is_the_call(what):
             return cider.cider_w8a8_gemm_pc_q(x, sx, w, sw, y=out, stream=st)
         like = torch.empty((200, 264), dtype=torch.float16, device="cuda")
     try:
-        want, out = call(torch.zeros_like(like), stream), torch.zeros_like(like)
+        want, out = torch.zeros_like(like), torch.zeros_like(like)
+        torch.cuda.synchronize()
+        call(want, stream)
         torch.cuda.synchronize()
         _at_once([lambda: call(out, stream)], 1)
         assert torch.equal(out, want)
